@@ -316,6 +316,60 @@ WKV_API int wkv_mstate_forward(int64_t B, int64_t T, int64_t H, int64_t N, const
                                const float* s0, float* s1, cudaStream_t stream);
 
 /*
+ * The gated delta rule: a matrix state per head with one decay and one write strength per
+ * token and head, the single-decay, single-key form of the delta-rule update that the
+ * research report "RWKV模型深度研究报告（截至2026年初）", section 1.3.3, generalises
+ * (wkv7_forward with w = e^g in every channel, a = -e^g k, b = beta k, and beta k as its key).
+ * Per head, with S[i][j] (value channel i, key channel j):
+ *   e_t = v_t - e^{g_t} S_{t-1} k_t
+ *   S_t = e^{g_t} S_{t-1} + beta_t e_t k_t^T
+ *   y_t = scale S_t q_t
+ * H value heads share Hk query/key heads: value head h reads query/key head h / (H / Hk).
+ *   q, k: (B, T, Hk, N); v, y: (B, T, H, N), in the problem's dtype, dense row-major.
+ *   g, beta: fp32 (B, T, H). g is the natural logarithm of the decay (g <= 0 in a model that
+ *     forgets; values below -200, -inf among them, act as a decay of zero).
+ *   states: fp32 (sequences, H, N, N), S[i][j] at i N + j.
+ * Sequences: the B batch rows of T tokens, or, with seq_offsets, n_seqs sequences packed into
+ * one row (B = 1): seq_offsets is a device array of n_seqs + 1 int32 token offsets, sequence s
+ * the tokens [seq_offsets[s], seq_offsets[s + 1]). Offsets are clamped to [0, T] and a
+ * sequence that ends before it starts is empty; sequences must not overlap. Tokens that no
+ * sequence covers are not read, and their rows of the outputs stay as they were.
+ * N must be 64 or 128 and Hk must divide H (else WKV_ERR_UNSUPPORTED); q, k, v, y and the
+ * states must be 16-byte aligned, g, beta and seq_offsets 4-byte (else WKV_ERR_ALIGNMENT).
+ * Stable for |beta_t| |k_t|^2 <= 2 (keys are unit vectors in a model). Inputs finite (but g,
+ * above): a value that is not reaches the tokens of its own 16-token group and all later ones.
+ */
+typedef enum wkv_dtype { WKV_DTYPE_F32 = 0, WKV_DTYPE_BF16 = 1 } wkv_dtype;
+
+typedef struct wkv_gdr_problem {
+  int64_t B, T, Hk, H, N;
+  int64_t n_seqs;             /* read only with seq_offsets */
+  const int32_t* seq_offsets; /* device, n_seqs + 1; NULL: the B rows are the sequences */
+  int dtype;                  /* wkv_dtype of q, k, v, y and their gradients */
+  float scale;
+} wkv_gdr_problem;
+
+/*
+ * Forward. s0: the initial states (NULL = zero); s1: the final states (NULL = not wanted;
+ * may alias s0). No tokens: s1 = s0. y must not overlap the inputs. Nothing is allocated.
+ */
+WKV_API int wkv_gdr_forward(const wkv_gdr_problem* p, const void* q, const void* k,
+                            const void* v, const float* g, const float* beta, void* y,
+                            const float* s0, float* s1, cudaStream_t stream);
+
+/*
+ * One token for each of n rows, the states updated in place: q, k (n, Hk, N); v, y (n, H, N);
+ * g, beta (n, H); p->B = n, p->T = 1, no seq_offsets. state: (n_slots, H, N, N). slots: device,
+ * n int32, the state of each row; NULL = row i has state i (n_slots >= n). A row whose slot is
+ * outside [0, n_slots) is padding: nothing of it is read and its y stays as it was. No two rows
+ * may name the same slot (the order of their updates would be open).
+ */
+WKV_API int wkv_gdr_decode_step(const wkv_gdr_problem* p, const void* q, const void* k,
+                                const void* v, const float* g, const float* beta, void* y,
+                                float* state, int64_t n_slots, const int32_t* slots,
+                                cudaStream_t stream);
+
+/*
  * Query and clear device-side errors. Synchronises `stream`, then returns WKV_ERR_TIMEOUT
  * if any kernel of this library on the current device gave up a bounded wait since the
  * last query, else WKV_ERR_RANGE if a kernel met an input outside its range (the outputs

@@ -15,7 +15,9 @@ __all__ = ["wkv_forward", "wkv_forward_bf16", "wkv_forward_state", "wkv_decode_s
            "wkv_decode_steps",
            "wkv_backward", "wkv_backward_state", "wkv_backward_workspace_bytes",
            "wkv_forward_checkpointed", "wkv_backward_checkpointed",
-           "wkv7_forward", "wkv_mstate_forward", "wkv_stream_status", "wkv_status_string", "WkvError", "lib",
+           "wkv7_forward", "wkv_mstate_forward",
+           "wkv_gdr_forward", "wkv_gdr_decode_step",
+           "wkv_stream_status", "wkv_status_string", "WkvError", "lib",
            "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libwkv.so")
@@ -53,6 +55,8 @@ _SIGS = {
     "wkv_testing_lookback_timeout": ([ctypes.c_uint64, _P], ctypes.c_int),
     "wkv_testing_backward_timeout": ([ctypes.c_uint64, _P], ctypes.c_int),
     "wkv_testing_forward_plain": ([_I, _I, _I] + [_P] * 6 + [ctypes.c_int, _P], ctypes.c_int),
+    "wkv_gdr_forward": ([_P] * 9 + [_P], ctypes.c_int),
+    "wkv_gdr_decode_step": ([_P] * 8 + [_I, _P, _P], ctypes.c_int),
     "wkv_testing_set_backward_path": ([ctypes.c_int], ctypes.c_int),
     "wkv_testing_pipe_rate": ([ctypes.c_int, _I, ctypes.POINTER(ctypes.c_double), _P],
                               ctypes.c_int),
@@ -435,3 +439,17 @@ def wkv_mstate_forward(r, w, k, v, state=None, y=None, state_out=None, want_stat
 def wkv_stream_status(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device-side status code."""
     return int(lib.wkv_stream_status(_stream(stream)))
+
+
+# Entry points whose binding is in a module of its own, which imports torch: loaded when first
+# used, so that importing the package (and loading the library) needs no torch.
+_IN_MODULES = {"wkv_gdr_forward": "gdr", "wkv_gdr_decode_step": "gdr"}
+
+
+def __getattr__(name):
+    if name not in _IN_MODULES:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    module = importlib.import_module("." + _IN_MODULES[name], __name__)
+    value = globals()[name] = getattr(module, name)
+    return value

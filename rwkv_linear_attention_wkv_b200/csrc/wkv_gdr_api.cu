@@ -1,0 +1,99 @@
+// C-ABI entry points of the gated delta rule: argument checks, plan selection, launches.
+// Declarations and their documentation: include/wkv.h.
+#include <cstdint>
+
+#include "wkv_internal.h"
+
+namespace wkv {
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Sizes of a problem. WKV_OK with *empty set where there is nothing to index.
+int check_problem(const wkv_gdr_problem* p, bool* empty) {
+  *empty = false;
+  if (p == nullptr) return WKV_ERR_INVALID_ARG;
+  if (p->B < 0 || p->T < 0 || p->Hk < 0 || p->H < 0 || p->N < 0) return WKV_ERR_INVALID_ARG;
+  if (p->dtype != WKV_DTYPE_F32 && p->dtype != WKV_DTYPE_BF16) return WKV_ERR_INVALID_ARG;
+  const bool packed = p->seq_offsets != nullptr;
+  if (packed && (p->n_seqs < 0 || p->B != 1)) return WKV_ERR_INVALID_ARG;
+  if (!aligned(p->seq_offsets, 4)) return WKV_ERR_ALIGNMENT;
+  const int64_t seqs = packed ? p->n_seqs : p->B;
+  if (seqs == 0 || p->H == 0) {
+    *empty = true;
+    return WKV_OK;
+  }
+  if (p->N != 64 && p->N != 128) return WKV_ERR_UNSUPPORTED;
+  if (p->Hk == 0 || p->H % p->Hk != 0) return WKV_ERR_UNSUPPORTED;
+  // Tokens and heads are indexed in int32, elements in int64; a grid is 31 bits wide.
+  constexpr int64_t kMax = int64_t(1) << 31;
+  if (p->T >= kMax || p->H >= (int64_t(1) << 20) || p->B >= kMax || seqs >= kMax / 8 / p->H)
+    return WKV_ERR_UNSUPPORTED;
+  if (p->T > 0 && (p->B > (int64_t(1) << 40) / p->T ||
+                   p->B * p->T > INT64_MAX / 16 / (p->H * p->N)))
+    return WKV_ERR_UNSUPPORTED;
+  return WKV_OK;
+}
+
+GdrArgs args_of(const wkv_gdr_problem* p) {
+  GdrArgs a{};
+  a.B = int(p->B); a.T = int(p->T); a.Hk = int(p->Hk); a.H = int(p->H); a.N = int(p->N);
+  a.offsets = p->seq_offsets;
+  a.n_seqs = p->seq_offsets ? int(p->n_seqs) : a.B;
+  a.bf16 = p->dtype == WKV_DTYPE_BF16;
+  a.scale = p->scale;
+  return a;
+}
+
+int pass_state(const float* s0, float* s1, size_t bytes, cudaStream_t stream) {
+  if (s1 == nullptr || s1 == s0) return WKV_OK;
+  const cudaError_t e = s0 ? cudaMemcpyAsync(s1, s0, bytes, cudaMemcpyDeviceToDevice, stream)
+                           : cudaMemsetAsync(s1, 0, bytes, stream);
+  return e == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+WKV_API int wkv_gdr_forward(const wkv_gdr_problem* p, const void* q, const void* k,
+                            const void* v, const float* g, const float* beta, void* y,
+                            const float* s0, float* s1, cudaStream_t stream) {
+  bool empty;
+  if (int rc = check_problem(p, &empty)) return rc;
+  if (empty) return WKV_OK;
+  if (p->T > 0 && (!q || !k || !v || !g || !beta || !y)) return WKV_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, (const void*)y, (const void*)s0, (const void*)s1})
+    if (!aligned(x, 16)) return WKV_ERR_ALIGNMENT;
+  if (!aligned(g, 4) || !aligned(beta, 4)) return WKV_ERR_ALIGNMENT;
+  GdrArgs a = args_of(p);
+  if (a.T == 0) return pass_state(s0, s1, size_t(a.n_seqs) * a.H * a.N * a.N * 4, stream);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.y = y; a.s0 = s0; a.s1 = s1;
+  return launch_gdr_recurrent(a, stream);
+}
+
+WKV_API int wkv_gdr_decode_step(const wkv_gdr_problem* p, const void* q, const void* k,
+                                const void* v, const float* g, const float* beta, void* y,
+                                float* state, int64_t n_slots, const int32_t* slots,
+                                cudaStream_t stream) {
+  bool empty;
+  if (int rc = check_problem(p, &empty)) return rc;
+  if (p->T != 1 || p->seq_offsets != nullptr || n_slots < 0) return WKV_ERR_INVALID_ARG;
+  if (empty) return WKV_OK;
+  if (!q || !k || !v || !g || !beta || !y || !state) return WKV_ERR_INVALID_ARG;
+  if (slots == nullptr && n_slots < p->B) return WKV_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, (const void*)y, (const void*)state})
+    if (!aligned(x, 16)) return WKV_ERR_ALIGNMENT;
+  if (!aligned(g, 4) || !aligned(beta, 4) || !aligned(slots, 4)) return WKV_ERR_ALIGNMENT;
+  if (n_slots >= (int64_t(1) << 31)) return WKV_ERR_UNSUPPORTED;
+  GdrArgs a = args_of(p);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.y = y; a.s0 = state; a.s1 = state;
+  a.n_slots = int(n_slots);
+  a.slots = slots;
+  return launch_gdr_recurrent(a, stream);
+}
+
+}  // extern "C"
+
+}  // namespace wkv

@@ -142,4 +142,26 @@ int launch_wkv7(int64_t B, int64_t T, int64_t H, const float* r, const float* w,
                 const float* v, const float* a, const float* b, float* y, const float* s0,
                 float* s1, unsigned* err, cudaStream_t stream);
 
+// Gated delta rule (wkv_gdr_*.cu). Sequences are batch rows, or spans of one packed row.
+struct GdrArgs {
+  int B, T, Hk, H, N;
+  int n_seqs;               // batch rows, or packed sequences
+  const int32_t* offsets;   // packed: n_seqs + 1 token offsets (device), else null
+  bool bf16;
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  void* y;
+  const float* s0;
+  float* s1;
+  // decode: states picked by slot
+  int n_slots = 0;
+  const int32_t* slots = nullptr;
+};
+// Token by token, the state in registers.
+int launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream);
+
 }  // namespace wkv

@@ -1,0 +1,127 @@
+"""The gated delta rule without a GPU: the 64-bit reference of the GPU tests against the C oracle
+and differences, and the refusals of the C entry points and of the binding."""
+import ctypes
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import gdr_reference as ref  # noqa: E402
+import oracle  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def W():
+    import rwkv_linear_attention_wkv_b200 as W
+    return W
+
+
+def test_reference_is_the_generalised_delta_rule():
+    # wkv7's update with w = e^g, a = -e^g k, b = beta k and beta k as its key
+    T, H, N = 37, 3, 64
+    q, k, v, g, beta = ref.inputs((T,), H, H, N, torch.float32, 1)
+    S0 = 0.3 * torch.randn(H, N, N, generator=torch.Generator().manual_seed(2))
+    y, S = ref.rule(q, k, v, g, beta, 0.125, S0)
+    d = lambda x: x.double().numpy()[None]  # noqa: E731
+    al = np.exp(d(g))[..., None]
+    bk = d(beta)[..., None] * d(k)
+    yo, So = oracle.wkv7_recurrent(0.125 * d(q), np.broadcast_to(al, d(k).shape).copy(), bk, d(v),
+                                   -al * d(k), bk, S0.double().numpy()[None], want_state=True)
+    assert np.abs(y.numpy() - yo[0]).max() < 1e-12
+    assert np.abs(S.numpy() - So[0]).max() < 1e-12
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "g", "beta", "state"])
+def test_reference_gradients_are_differences(name):
+    T, Hk, H, N = 7, 2, 4, 8
+    gen = torch.Generator().manual_seed(3)
+    x = dict(zip(("q", "k", "v", "g", "beta"), (t.double() for t in ref.inputs(
+        (T,), Hk, H, N, torch.float64, 4))))
+    x["state"] = torch.randn(H, N, N, generator=gen, dtype=torch.float64)
+    dy = torch.randn(T, H, N, generator=gen, dtype=torch.float64)
+    dS = torch.randn(H, N, N, generator=gen, dtype=torch.float64)
+    got = ref.rule_gradients(**{n: x[n] for n in ("q", "k", "v", "g", "beta")}, scale=0.7, dy=dy,
+                             state=x["state"], dstate=dS)["d" + name]
+
+    def loss(z):
+        y, S = ref.rule(z["q"], z["k"], z["v"], z["g"], z["beta"], 0.7, z["state"])
+        return float((y * dy).sum() + (S * dS).sum())
+
+    pick = torch.randperm(x[name].numel(), generator=gen)[:12]
+    for i in pick.tolist():
+        far = []
+        for s in (1e-5, -1e-5):
+            z = dict(x)
+            z[name] = x[name].clone()
+            z[name].view(-1)[i] += s
+            far.append(loss(z))
+        assert abs((far[0] - far[1]) / 2e-5 - float(got.reshape(-1)[i])) < 1e-6
+
+
+def problem(W, **over):
+    from rwkv_linear_attention_wkv_b200.gdr import GdrProblem
+    x = dict(B=2, T=5, Hk=2, H=4, N=64, n_seqs=0, seq_offsets=None, dtype=1, scale=1.0)
+    x.update(over)
+    return ctypes.byref(GdrProblem(*[x[n] for n, _ in GdrProblem._fields_]))
+
+
+def test_forward_refusals(W):
+    f, ok = W.lib.wkv_gdr_forward, 4096
+    args = [ok] * 6 + [None, None, None]
+    call = lambda over={}, **at: f(problem(W, **over),  # noqa: E731
+                                   *[at.get("p%d" % i, x) for i, x in enumerate(args)])
+    assert f(None, *args) == 1
+    for over in (dict(B=-1), dict(T=-1), dict(H=-1), dict(Hk=-1), dict(N=-64), dict(dtype=2),
+                 dict(seq_offsets=ok, n_seqs=-1, B=1), dict(seq_offsets=ok, n_seqs=2, B=2)):
+        assert call(over) == 1, over
+    for over in (dict(N=32), dict(N=96), dict(H=5), dict(Hk=0), dict(T=1 << 31), dict(B=1 << 31),
+                 dict(H=1 << 20, Hk=1), dict(seq_offsets=ok, B=1, n_seqs=1 << 30)):
+        assert call(over) == 5, over
+    assert call(dict(seq_offsets=ok + 2, B=1, n_seqs=2)) == 2
+    for i in range(6):
+        assert call(**{"p%d" % i: None}) == 1, i
+    for i in (0, 1, 2, 5, 6, 7):
+        assert call(**{"p%d" % i: ok + 8}) == 2, i
+    for i in (3, 4):
+        assert call(**{"p%d" % i: ok + 2}) == 2, i
+    assert call(dict(B=0)) == 0 and call(dict(H=0)) == 0
+    assert call(dict(seq_offsets=ok, B=1, n_seqs=0)) == 0
+    assert call(dict(T=0)) == 0  # no tokens and no final state wanted
+
+
+def test_decode_refusals(W):
+    f, ok = W.lib.wkv_gdr_decode_step, 4096
+    args = [ok] * 7
+
+    def call(over={}, n_slots=2, slots=None, **at):
+        return f(problem(W, **{"T": 1, **over}), *[at.get("p%d" % i, x) for i, x in enumerate(args)],
+                 n_slots, slots, None)
+
+    assert call(dict(T=2)) == 1 and call(dict(T=0)) == 1
+    assert call(dict(seq_offsets=ok, B=1, n_seqs=1)) == 1
+    assert call(n_slots=1) == 1 and call(n_slots=-1) == 1
+    for i in range(7):
+        assert call(**{"p%d" % i: None}) == 1, i
+    for i in (0, 1, 2, 5, 6):
+        assert call(**{"p%d" % i: ok + 8}) == 2, i
+    assert call(slots=ok + 2) == 2
+    assert call(dict(N=48)) == 5 and call(slots=ok, n_slots=1 << 31) == 5
+    assert call(dict(B=0), n_slots=0) == 0
+
+
+def test_binding_refusals(W):
+    q = torch.zeros(1, 2, 3, 64)
+    g = torch.zeros(1, 2, 3)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        W.wkv_gdr_forward(q, q, q, g, g)
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        W.wkv_gdr_forward(q.numpy(), q, q, g, g)
+    with pytest.raises(TypeError, match="float32 or torch.bfloat16"):
+        W.wkv_gdr_forward(q, q, q.half(), g, g)
+    with pytest.raises(ValueError, match="4 dimensions"):
+        W.wkv_gdr_forward(q[0], q[0], q[0], g, g)
+    with pytest.raises(ValueError, match="3 dimensions"):
+        W.wkv_gdr_decode_step(q, q, q, g, g, q)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        W.wkv_gdr_decode_step(q[0], q[0], q[0], g[0], g[0], torch.zeros(2, 3, 64, 64))
