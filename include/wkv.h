@@ -370,6 +370,52 @@ WKV_API int wkv_gdr_decode_step(const wkv_gdr_problem* p, const void* q, const v
                                 cudaStream_t stream);
 
 /*
+ * What surrounds a time-mixing block: the norm and gate of its read-out (the concept page's
+ * section 3.2 gates the read-out by the receptance; matrix-valued states are normed per head
+ * first), the scaled residual, and the norm that the next block reads. Per row of C channels,
+ * RMS(u) = sqrt(mean(u^2) + eps) over each group of channels for h and over the row for out:
+ *   m   = act(gate) weight h / RMS_group(h)
+ *   out = x + scale m            (x NULL: out = m)
+ *   y   = next_weight out / RMS_row(out)
+ * h, gate, x, out, y: (R, C) dense row-major in the problem's dtype; weight, scale,
+ * next_weight: fp32 [C]. Any of these may be left out (NULL): gate (act(gate) = 1; act is then
+ * not read), weight (ones), x, scale (ones; only with x), next_weight with y (not wanted).
+ * y is made from the unrounded out. out may be h or x itself; y must not overlap the others.
+ * group divides C (a head, or C). C up to 8192 (else WKV_ERR_UNSUPPORTED). Any alignment of an
+ * element; rows of a multiple of 8 channels in 16-byte aligned arrays are read by vectors.
+ */
+typedef enum wkv_act { WKV_ACT_NONE = 0, WKV_ACT_SIGMOID = 1, WKV_ACT_SILU = 2 } wkv_act;
+
+typedef struct wkv_norm_gate_problem {
+  int64_t R, C, group;
+  int dtype; /* wkv_dtype */
+  int act;   /* wkv_act of the gate */
+  float eps; /* > 0 */
+} wkv_norm_gate_problem;
+
+WKV_API int wkv_norm_gate_forward(const wkv_norm_gate_problem* p, const void* h,
+                                  const float* weight, const void* gate, const void* x,
+                                  const float* scale, const float* next_weight, void* out,
+                                  void* y, cudaStream_t stream);
+
+/*
+ * Gradients of sum(dout out) + sum(dy y), everything recomputed from the forward's inputs. dout
+ * or dy may be NULL (zero), not both; dy only with next_weight. dh is written always; dweight,
+ * dgate (with gate), dx (with x), dscale (with x and scale) and dnext_weight (with dy) where
+ * they are not NULL. dh, dgate and dx must not overlap the inputs or one another. Sums over
+ * rows are fp32 in a fixed order (the same from call to call on one GPU model). workspace:
+ * device, 16-byte aligned, wkv_norm_gate_workspace_bytes(R, C) bytes, scratch. R == 0: dweight,
+ * dscale and dnext_weight are zeroed.
+ */
+WKV_API size_t wkv_norm_gate_workspace_bytes(int64_t R, int64_t C);
+WKV_API int wkv_norm_gate_backward(const wkv_norm_gate_problem* p, const void* h,
+                                   const float* weight, const void* gate, const void* x,
+                                   const float* scale, const float* next_weight,
+                                   const void* dout, const void* dy, void* dh, float* dweight,
+                                   void* dgate, void* dx, float* dscale, float* dnext_weight,
+                                   void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Query and clear device-side errors. Synchronises `stream`, then returns WKV_ERR_TIMEOUT
  * if any kernel of this library on the current device gave up a bounded wait since the
  * last query, else WKV_ERR_RANGE if a kernel met an input outside its range (the outputs

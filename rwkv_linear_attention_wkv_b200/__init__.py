@@ -17,6 +17,7 @@ __all__ = ["wkv_forward", "wkv_forward_bf16", "wkv_forward_state", "wkv_decode_s
            "wkv_forward_checkpointed", "wkv_backward_checkpointed",
            "wkv7_forward", "wkv_mstate_forward",
            "wkv_gdr_forward", "wkv_gdr_decode_step",
+           "wkv_norm_gate_forward", "wkv_norm_gate_backward", "wkv_norm_gate_workspace_bytes",
            "wkv_stream_status", "wkv_status_string", "WkvError", "lib",
            "LIB_PATH"]
 
@@ -57,6 +58,9 @@ _SIGS = {
     "wkv_testing_forward_plain": ([_I, _I, _I] + [_P] * 6 + [ctypes.c_int, _P], ctypes.c_int),
     "wkv_gdr_forward": ([_P] * 9 + [_P], ctypes.c_int),
     "wkv_gdr_decode_step": ([_P] * 8 + [_I, _P, _P], ctypes.c_int),
+    "wkv_norm_gate_forward": ([_P] * 9 + [_P], ctypes.c_int),
+    "wkv_norm_gate_workspace_bytes": ([_I, _I], ctypes.c_size_t),
+    "wkv_norm_gate_backward": ([_P] * 16 + [ctypes.c_size_t, _P], ctypes.c_int),
     "wkv_testing_set_backward_path": ([ctypes.c_int], ctypes.c_int),
     "wkv_testing_pipe_rate": ([ctypes.c_int, _I, ctypes.POINTER(ctypes.c_double), _P],
                               ctypes.c_int),
@@ -443,7 +447,9 @@ def wkv_stream_status(stream=None) -> int:
 
 # Entry points whose binding is in a module of its own, which imports torch: loaded when first
 # used, so that importing the package (and loading the library) needs no torch.
-_IN_MODULES = {"wkv_gdr_forward": "gdr", "wkv_gdr_decode_step": "gdr"}
+_IN_MODULES = {"wkv_gdr_forward": "gdr", "wkv_gdr_decode_step": "gdr",
+               "wkv_norm_gate_forward": "norm_gate", "wkv_norm_gate_backward": "norm_gate",
+               "wkv_norm_gate_workspace_bytes": "norm_gate"}
 
 
 def __getattr__(name):

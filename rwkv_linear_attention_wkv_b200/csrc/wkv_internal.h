@@ -164,4 +164,35 @@ struct GdrArgs {
 // Token by token, the state in registers.
 int launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream);
 
+// Norm, gate, residual and next norm around a block (wkv_norm_gate.cu); null pointers are what
+// the entry points let a caller leave out.
+struct NormGateArgs {
+  int64_t R;
+  int C, group, act;
+  bool bf16;
+  float eps;
+  const void* h;
+  const float* weight;
+  const void* gate;
+  const void* x;
+  const float* scale;
+  const float* next_weight;
+  void* out;
+  void* y;
+  // backward
+  const void* dout = nullptr;
+  const void* dy = nullptr;
+  void* dh = nullptr;
+  float* dweight = nullptr;
+  void* dgate = nullptr;
+  void* dx = nullptr;
+  float* dscale = nullptr;
+  float* dnext_weight = nullptr;
+  float* partial = nullptr;  // norm_gate_workspace_bytes(R, C)
+};
+int64_t norm_gate_max_c();
+size_t norm_gate_workspace_bytes(int64_t R, int64_t C);
+int launch_norm_gate_forward(const NormGateArgs& a, cudaStream_t stream);
+int launch_norm_gate_backward(const NormGateArgs& a, cudaStream_t stream);
+
 }  // namespace wkv

@@ -1,0 +1,473 @@
+// Norm, gate, scaled residual and next norm around a block, forward and backward (sm_100a).
+//
+// Per row of C channels, r1 = 1 / RMS over a group of channels, r2 = 1 / RMS over the row:
+//   m   = act(z) w h r1,   out = x + s m,   y = w' out r2.
+// Backward, with d = dout + r2 (dy w' - out r2^2 <dy w', out> / C):
+//   dx = d,  ds = sum_rows d m,  dz = d s w h r1 act'(z),  dw = sum_rows d s act(z) h r1,
+//   dh = r1 (n - h r1^2 <n, h>_group / group),  n = d s act(z) w,   dw' = sum_rows dy out r2.
+//
+// A team of ceil(C / 256) warps holds a row, eight channels a thread, and walks rows; a thread
+// meets the same channels in every row, so the three weights stay in its registers, as do its
+// sums of dw, ds and dw' (one line per team into the workspace at the end, added up in a fixed
+// order by a second kernel). The next row's inputs are loaded before this row's sums, so that a
+// row is always in flight: bound by HBM. Group sums are shuffles where a group is 8 x a power of
+// two channels up to 256 (the heads), the row sum where it is the row, and go through shared
+// memory otherwise.
+#include <algorithm>
+
+#include "wkv_device.cuh"
+#include "wkv_internal.h"
+
+namespace wkv {
+
+namespace {
+
+constexpr int kE = 8;             // channels per thread
+constexpr int kMaxC = 8192;       // 1024 threads a row
+constexpr int kTeamsMax = 8;      // rows a CTA works on at once
+
+enum GroupMode { kRow, kLanes, kAny };
+
+struct Eight {
+  float v[kE];
+};
+
+// Raw values as loaded (four or eight registers), so that a prefetched row costs little.
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+  float4 a, b;
+};
+template <> struct Raw<__nv_bfloat16> {
+  uint4 a;
+};
+
+// Where a thread's eight channels are: adjacent (VEC), or a row's width apart (any C, any
+// alignment).
+template <bool VEC>
+struct Place {
+  int c0, step, C;
+  __device__ int at(int i) const { return VEC ? c0 + i : c0 + i * step; }
+  __device__ bool in(int i) const { return VEC ? c0 < C : c0 + i * step < C; }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw<T> load_raw(const T* p, const Place<VEC>& pl) {
+  Raw<T> r;
+  T* e = reinterpret_cast<T*>(&r);
+  if (VEC) {
+    if (pl.c0 < pl.C) {
+      r = *reinterpret_cast<const Raw<T>*>(p + pl.c0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) e[i] = Elem<T>::from_f(0.f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kE; ++i) e[i] = pl.in(i) ? p[pl.at(i)] : Elem<T>::from_f(0.f);
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ Eight widen(const Raw<T>& r) {
+  const T* e = reinterpret_cast<const T*>(&r);
+  Eight x;
+#pragma unroll
+  for (int i = 0; i < kE; ++i) x.v[i] = Elem<T>::to_f(e[i]);
+  return x;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store(T* p, const Eight& x, const Place<VEC>& pl) {
+  Raw<T> r;
+  T* e = reinterpret_cast<T*>(&r);
+#pragma unroll
+  for (int i = 0; i < kE; ++i) e[i] = Elem<T>::from_f(x.v[i]);
+  if (VEC) {
+    if (pl.c0 < pl.C) *reinterpret_cast<Raw<T>*>(p + pl.c0) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kE; ++i)
+      if (pl.in(i)) p[pl.at(i)] = e[i];
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ Eight params(const float* p, const Place<VEC>& pl, float none) {
+  Eight x;
+#pragma unroll
+  for (int i = 0; i < kE; ++i) x.v[i] = !pl.in(i) ? 0.f : p ? p[pl.at(i)] : none;
+  return x;
+}
+
+// The warps that hold one row: their sums go through shared memory (two slots in turn, so that
+// one barrier a sum is enough).
+struct Team {
+  int warps, warp, lane, id;
+  float2* slots;     // [2][32]
+  float* parts;      // kAny: one value per channel (VEC: per eight) and one per group
+  int turn = 0;
+
+  __device__ void sync() const {
+    if (warps == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(warps * 32) : "memory");
+  }
+
+  __device__ float2 sum(float a, float b) {
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, m);
+      b += __shfl_xor_sync(0xffffffffu, b, m);
+    }
+    if (warps == 1) return make_float2(a, b);
+    float2* s = slots + 32 * turn;
+    turn ^= 1;
+    if (lane == 0) s[warp] = make_float2(a, b);
+    sync();
+    a = b = 0.f;
+    for (int w = 0; w < warps; ++w) {
+      a += s[w].x;
+      b += s[w].y;
+    }
+    return make_float2(a, b);
+  }
+};
+
+// For each of a thread's channels the sum of x over the channel's group.
+template <bool VEC, GroupMode MODE>
+__device__ __forceinline__ Eight group_sum(const Eight& x, Team& t, const Place<VEC>& pl,
+                                           int group) {
+  Eight out;
+  if (MODE != kAny) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) s += x.v[i];
+    if (MODE == kRow) {
+      s = t.sum(s, 0.f).x;
+    } else {
+      for (int m = group / kE / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    }
+#pragma unroll
+    for (int i = 0; i < kE; ++i) out.v[i] = s;
+    return out;
+  }
+  float* sums = t.parts + pl.C;
+  t.sync();  // the last sums have been read
+#pragma unroll
+  for (int i = 0; i < kE; ++i)
+    if (pl.in(i)) t.parts[pl.at(i)] = x.v[i];
+  t.sync();
+  for (int g = t.warp; g < pl.C / group; g += t.warps) {
+    float s = 0.f;
+    for (int c = t.lane; c < group; c += 32) s += t.parts[g * group + c];
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (t.lane == 0) sums[g] = s;
+  }
+  t.sync();
+#pragma unroll
+  for (int i = 0; i < kE; ++i) out.v[i] = pl.in(i) ? sums[pl.at(i) / group] : 0.f;
+  return out;
+}
+
+// act(z) and its slope; act: 0 none, 1 sigmoid, 2 silu.
+__device__ __forceinline__ void gate_of(float z, int act, float& a, float& slope) {
+  const float s = 1.f / (1.f + expf(-z)), d = s * (1.f - s);
+  a = act == WKV_ACT_SILU ? z * s : s;
+  slope = act == WKV_ACT_SILU ? fmaf(z, d, s) : d;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void make_team(int team_warps, int C, Team& t, Place<VEC>& pl) {
+  extern __shared__ float smem_ng[];
+  const int warp = threadIdx.x >> 5;
+  t.warps = team_warps;
+  t.id = warp / team_warps;
+  t.warp = warp % team_warps;
+  t.lane = threadIdx.x & 31;
+  const int teams = (blockDim.x >> 5) / team_warps;
+  t.slots = reinterpret_cast<float2*>(smem_ng) + 64 * t.id;
+  t.parts = smem_ng + 128 * teams + 2 * C * t.id;
+  const int at = t.warp * 32 + t.lane;
+  pl.C = C;
+  pl.step = team_warps * 32;
+  pl.c0 = VEC ? at * kE : at;
+}
+
+template <typename T, bool VEC, GroupMode MODE, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_fwd_kernel(NormGateArgs a, int team_warps) {
+  Team t;
+  Place<VEC> pl;
+  make_team<VEC>(team_warps, a.C, t, pl);
+  const int teams = (blockDim.x >> 5) / team_warps;
+  const Eight w = params(a.weight, pl, 1.f), s = params(a.scale, pl, 1.f),
+              wn = params(a.next_weight, pl, 1.f);
+  const T *h = static_cast<const T*>(a.h), *z = static_cast<const T*>(a.gate),
+          *x = static_cast<const T*>(a.x);
+  const float inv_group = 1.f / a.group, inv_c = 1.f / a.C;
+  int64_t row = int64_t(blockIdx.x) * teams + t.id;
+  const int64_t stride = int64_t(gridDim.x) * teams;
+  Raw<T> hr, zr, xr;
+  auto fetch = [&](int64_t r) {
+    hr = load_raw<T, VEC>(h + r * a.C, pl);
+    if (z) zr = load_raw<T, VEC>(z + r * a.C, pl);
+    if (x) xr = load_raw<T, VEC>(x + r * a.C, pl);
+  };
+  if (row < a.R) fetch(row);
+  for (; row < a.R; row += stride) {
+    const Eight hv = widen<T>(hr);
+    Eight m;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) m.v[i] = hv.v[i] * w.v[i];
+    if (z) {
+      const Eight zv = widen<T>(zr);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        float act, slope;
+        gate_of(zv.v[i], a.act, act, slope);
+        m.v[i] *= act;
+      }
+    }
+    Eight xv{};
+    if (x) xv = widen<T>(xr);
+    if (row + stride < a.R) fetch(row + stride);
+    Eight sq;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) sq.v[i] = hv.v[i] * hv.v[i];
+    const Eight ms = group_sum<VEC, MODE>(sq, t, pl, a.group);
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      m.v[i] *= rsqrtf(fmaf(ms.v[i], inv_group, a.eps));
+      if (x) m.v[i] = fmaf(s.v[i], m.v[i], xv.v[i]);
+    }
+    store<T, VEC>(static_cast<T*>(a.out) + row * a.C, m, pl);
+    if (a.y) {
+      float q = 0.f;
+#pragma unroll
+      for (int i = 0; i < kE; ++i) q = fmaf(m.v[i], m.v[i], q);
+      const float r2 = rsqrtf(fmaf(t.sum(q, 0.f).x, inv_c, a.eps));
+#pragma unroll
+      for (int i = 0; i < kE; ++i) m.v[i] *= r2 * wn.v[i];
+      store<T, VEC>(static_cast<T*>(a.y) + row * a.C, m, pl);
+    }
+  }
+}
+
+template <typename T, bool VEC, GroupMode MODE, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_bwd_kernel(NormGateArgs a, int team_warps) {
+  Team t;
+  Place<VEC> pl;
+  make_team<VEC>(team_warps, a.C, t, pl);
+  const int teams = (blockDim.x >> 5) / team_warps;
+  const Eight w = params(a.weight, pl, 1.f), s = params(a.scale, pl, 1.f),
+              wn = params(a.next_weight, pl, 1.f);
+  const T *h = static_cast<const T*>(a.h), *z = static_cast<const T*>(a.gate),
+          *x = static_cast<const T*>(a.x), *dout = static_cast<const T*>(a.dout),
+          *dy = static_cast<const T*>(a.dy);
+  const float inv_group = 1.f / a.group, inv_c = 1.f / a.C;
+  const int64_t first = int64_t(blockIdx.x) * teams + t.id;
+  const int64_t stride = int64_t(gridDim.x) * teams;
+  Eight dw{}, ds{}, dwn{};
+  Raw<T> hr, zr, xr, dor, dyr;
+  auto fetch = [&](int64_t r) {
+    hr = load_raw<T, VEC>(h + r * a.C, pl);
+    if (z) zr = load_raw<T, VEC>(z + r * a.C, pl);
+    if (x) xr = load_raw<T, VEC>(x + r * a.C, pl);
+    if (dout) dor = load_raw<T, VEC>(dout + r * a.C, pl);
+    if (dy) dyr = load_raw<T, VEC>(dy + r * a.C, pl);
+  };
+  if (first < a.R) fetch(first);
+  for (int64_t row = first; row < a.R; row += stride) {
+    Eight hn = widen<T>(hr), act, slope, d{}, out{};
+#pragma unroll
+    for (int i = 0; i < kE; ++i) act.v[i] = 1.f;
+    if (z) {
+      const Eight zv = widen<T>(zr);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) gate_of(zv.v[i], a.act, act.v[i], slope.v[i]);
+    }
+    if (x) out = widen<T>(xr);
+    if (dout) d = widen<T>(dor);
+    Eight dn{};
+    if (dy) dn = widen<T>(dyr);
+    if (row + stride < a.R) fetch(row + stride);
+    Eight r1;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) r1.v[i] = hn.v[i] * hn.v[i];
+    r1 = group_sum<VEC, MODE>(r1, t, pl, a.group);
+    float so = 0.f, sd = 0.f;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      r1.v[i] = rsqrtf(fmaf(r1.v[i], inv_group, a.eps));
+      hn.v[i] *= r1.v[i];
+      out.v[i] = fmaf(s.v[i], act.v[i] * w.v[i] * hn.v[i], out.v[i]);
+      so = fmaf(out.v[i], out.v[i], so);
+      sd = fmaf(out.v[i], dn.v[i] * wn.v[i], sd);
+    }
+    if (dy) {
+      const float2 both = t.sum(so, sd);
+      const float r2 = rsqrtf(fmaf(both.x, inv_c, a.eps));
+      const float pull = r2 * r2 * both.y * inv_c;  // <dy w', out r2> r2 / C
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        dwn.v[i] = fmaf(dn.v[i], out.v[i] * r2, dwn.v[i]);
+        d.v[i] += r2 * (dn.v[i] * wn.v[i] - out.v[i] * pull);
+      }
+    }
+    if (a.dx) store<T, VEC>(static_cast<T*>(a.dx) + row * a.C, d, pl);
+    Eight n, p;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      const float dm = d.v[i] * s.v[i], ah = act.v[i] * hn.v[i];
+      ds.v[i] = fmaf(d.v[i], ah * w.v[i], ds.v[i]);
+      dw.v[i] = fmaf(dm, ah, dw.v[i]);
+      slope.v[i] = z ? dm * w.v[i] * hn.v[i] * slope.v[i] : 0.f;
+      n.v[i] = dm * act.v[i] * w.v[i];
+      p.v[i] = n.v[i] * hn.v[i];
+    }
+    if (a.dgate) store<T, VEC>(static_cast<T*>(a.dgate) + row * a.C, slope, pl);
+    p = group_sum<VEC, MODE>(p, t, pl, a.group);
+#pragma unroll
+    for (int i = 0; i < kE; ++i)
+      n.v[i] = r1.v[i] * fmaf(-hn.v[i], p.v[i] * inv_group, n.v[i]);
+    store<T, VEC>(static_cast<T*>(a.dh) + row * a.C, n, pl);
+  }
+  float* line = a.partial + first * 3 * a.C;  // [dw, ds, dw'] of this team
+#pragma unroll
+  for (int i = 0; i < kE; ++i)
+    if (pl.in(i)) {
+      line[pl.at(i)] = dw.v[i];
+      line[a.C + pl.at(i)] = ds.v[i];
+      line[2 * a.C + pl.at(i)] = dwn.v[i];
+    }
+}
+
+// The teams' lines added up: 32 columns x 8 slices of the lines a CTA, the slices in order.
+__global__ void __launch_bounds__(256) norm_gate_sum_kernel(const float* partial, int lines, int C,
+                                                            float* dw, float* ds, float* dwn) {
+  __shared__ float part[8][32];
+  float* const to = blockIdx.y == 0 ? dw : blockIdx.y == 1 ? ds : dwn;
+  if (to == nullptr) return;
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < C) {
+    const float* p = partial + int64_t(blockIdx.y) * C + c;
+#pragma unroll 8
+    for (int l = slice; l < lines; l += 8) s += p[int64_t(l) * 3 * C];
+  }
+  part[slice][lane] = s;
+  __syncthreads();
+  if (slice == 0 && c < C) {
+    for (int i = 1; i < 8; ++i) s += part[i][lane];
+    to[c] = s;
+  }
+}
+
+struct Plan {
+  int team_warps, teams, grid;
+  GroupMode mode;
+  size_t smem;
+};
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+// Threads of a CTA: rows of 256 channels or less four to a CTA, wider ones as many as make 384
+// threads; CTAs: enough for `threads` threads on every SM, each of whose teams has a row.
+Plan plan_of(int64_t R, int C, int group, bool vec, int threads, int sms) {
+  Plan p;
+  p.team_warps = (C + 32 * kE - 1) / (32 * kE);
+  p.teams = std::max(1, std::min(kTeamsMax, 12 / p.team_warps));
+  const int per_sm = std::max(1, threads / (32 * p.team_warps * p.teams));
+  p.grid = int(std::min<int64_t>((R + p.teams - 1) / p.teams, int64_t(sms) * per_sm));
+  const int lanes = group / kE;
+  const bool pow2 = (lanes & (lanes - 1)) == 0;
+  p.mode = group == C ? kRow
+           : vec && group % kE == 0 && lanes <= 32 && pow2 ? kLanes
+                                                           : kAny;
+  p.smem = size_t(p.teams) * (512 + (p.mode == kAny ? 8 * size_t(C) : 0));
+  return p;
+}
+
+constexpr int kFwdThreads = 1536, kBwdThreads = 768;
+
+// Rows of up to 4096 channels fit 512 threads, which leaves a thread the 128 registers that the
+// weights, the sums over rows and the next row need; wider ones take 1024 and spill some.
+template <typename T, bool VEC, GroupMode MODE>
+int run(const NormGateArgs& a, const Plan& p, bool backward, cudaStream_t stream) {
+  auto* kernel = p.team_warps * p.teams <= 16
+                     ? (backward ? norm_gate_bwd_kernel<T, VEC, MODE, 512>
+                                 : norm_gate_fwd_kernel<T, VEC, MODE, 512>)
+                     : (backward ? norm_gate_bwd_kernel<T, VEC, MODE, 1024>
+                                 : norm_gate_fwd_kernel<T, VEC, MODE, 1024>);
+  if (p.smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem)) !=
+          cudaSuccess)
+    return WKV_ERR_CUDA;
+  kernel<<<p.grid, p.team_warps * p.teams * 32, p.smem, stream>>>(a, p.team_warps);
+  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+}
+
+template <typename T>
+int pick(const NormGateArgs& a, const Plan& p, bool vec, bool backward, cudaStream_t stream) {
+  if (vec) {
+    if (p.mode == kRow) return run<T, true, kRow>(a, p, backward, stream);
+    if (p.mode == kLanes) return run<T, true, kLanes>(a, p, backward, stream);
+    return run<T, true, kAny>(a, p, backward, stream);
+  }
+  if (p.mode == kRow) return run<T, false, kRow>(a, p, backward, stream);
+  return run<T, false, kAny>(a, p, backward, stream);
+}
+
+bool vectors(const NormGateArgs& a) {
+  uintptr_t all = 0;
+  for (const void* q : {a.h, a.gate, a.x, (const void*)a.out, (const void*)a.y, a.dout, a.dy,
+                        (const void*)a.dh, (const void*)a.dgate, (const void*)a.dx})
+    all |= reinterpret_cast<uintptr_t>(q);
+  return a.C % kE == 0 && all % 16 == 0;
+}
+
+}  // namespace
+
+int64_t norm_gate_max_c() { return kMaxC; }
+
+// Lines of partial sums: no more teams than the widest grid has (a 160-SM bound, so that the
+// size does not depend on the device that is current).
+size_t norm_gate_workspace_bytes(int64_t R, int64_t C) {
+  if (R <= 0 || C <= 0 || C > kMaxC) return 0;
+  const Plan p = plan_of(R, int(C), int(C), true, kBwdThreads, 160);
+  return size_t(p.grid) * p.teams * 3 * size_t(C) * sizeof(float);
+}
+
+int launch_norm_gate_forward(const NormGateArgs& a, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return WKV_ERR_CUDA;
+  const bool vec = vectors(a);
+  const Plan p = plan_of(a.R, a.C, a.group, vec, kFwdThreads, sms);
+  return a.bf16 ? pick<__nv_bfloat16>(a, p, vec, false, stream)
+                : pick<float>(a, p, vec, false, stream);
+}
+
+int launch_norm_gate_backward(const NormGateArgs& a, cudaStream_t stream) {
+  const int sms = std::min(sm_count(), 160);
+  if (sms <= 0) return WKV_ERR_CUDA;
+  const bool vec = vectors(a);
+  const Plan p = plan_of(a.R, a.C, a.group, vec, kBwdThreads, sms);
+  const int rc = a.bf16 ? pick<__nv_bfloat16>(a, p, vec, true, stream)
+                        : pick<float>(a, p, vec, true, stream);
+  if (rc != WKV_OK) return rc;
+  if (!a.dweight && !a.dscale && !a.dnext_weight) return WKV_OK;
+  norm_gate_sum_kernel<<<dim3((a.C + 31) / 32, 3), 256, 0, stream>>>(
+      a.partial, p.grid * p.teams, a.C, a.dweight, a.dscale, a.dnext_weight);
+  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+}
+
+}  // namespace wkv

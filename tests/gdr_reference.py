@@ -111,3 +111,43 @@ def assert_close(got, ref, what, head_dim=None):
     err = (x - ref).abs()
     bad = ~(err <= bound)
     assert not bad.any(), (what, int(bad.sum()), float((err / bound).nan_to_num(9e9).max()))
+
+
+def norm_gate(h, weight, gate, x, scale, next_weight, group, act, eps):
+    """out and y of the norm around a block; everything (R, C) or (C,), None where left out."""
+    d = lambda t: None if t is None else t.double()  # noqa: E731
+    h, weight, gate, x, scale, next_weight = map(d, (h, weight, gate, x, scale, next_weight))
+    R, C = h.shape
+    hg = h.reshape(R, C // group, group)
+    m = (hg / torch.sqrt((hg ** 2).mean(-1, keepdim=True) + eps)).reshape(R, C)
+    if weight is not None:
+        m = m * weight
+    if gate is not None:
+        m = m * torch.sigmoid(gate) * (gate if act == "silu" else 1.0)
+    out = m if x is None else x + (m if scale is None else scale * m)
+    if next_weight is None:
+        return out, None
+    return out, out / torch.sqrt((out ** 2).mean(-1, keepdim=True) + eps) * next_weight
+
+
+NORM_NAMES = ("h", "weight", "gate", "x", "scale", "next_weight")
+
+
+def norm_gate_gradients(inputs, group, act, eps, dout, dy):
+    """Gradients by autograd in 64 bits, and for the sums over rows the sums of |terms|."""
+    leaves = {n: t.double().requires_grad_() for n, t in inputs.items() if t is not None}
+    out, y = norm_gate(*[leaves.get(n) for n in NORM_NAMES], group, act, eps)
+    per_row = torch.zeros(out.shape[0], dtype=torch.float64)
+    if dout is not None:
+        per_row = per_row + (out * dout.double()).sum(1)
+    if dy is not None:
+        per_row = per_row + (y * dy.double()).sum(1)
+    wanted = [n for n in leaves if not (n == "next_weight" and dy is None)]
+    grads = dict(zip(wanted, torch.autograd.grad(per_row.sum(), [leaves[n] for n in wanted],
+                                                 retain_graph=True)))
+    sums = {}
+    for n in ("weight", "scale", "next_weight"):
+        if n in grads:
+            sums[n] = sum(torch.autograd.grad(r, leaves[n], retain_graph=True)[0].abs()
+                          for r in per_row)
+    return grads, sums
