@@ -70,7 +70,7 @@ WKV_API int wkv_gdr_forward(const wkv_gdr_problem* p, const void* q, const void*
   GdrArgs a = args_of(p);
   if (a.T == 0) return pass_state(s0, s1, size_t(a.n_seqs) * a.H * a.N * a.N * 4, stream);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.y = y; a.s0 = s0; a.s1 = s1;
-  return launch_gdr_recurrent(a, stream);
+  return launch_gdr_chunked(a, nullptr, nullptr, stream);
 }
 
 WKV_API int wkv_gdr_decode_step(const wkv_gdr_problem* p, const void* q, const void* k,

@@ -163,6 +163,17 @@ struct GdrArgs {
 };
 // Token by token, the state in registers.
 int launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream);
+// In groups of 16 tokens on the matrix units. e (tokens, H, N) and checkpoints (chunks, H, N, N)
+// are what the backward reads: every token's error before its write, and the state entering
+// every chunk of kGdrChunk tokens of every sequence; null = not wanted.
+constexpr int kGdrChunk = 64;
+int launch_gdr_chunked(const GdrArgs& a, float* e, float* checkpoints, cudaStream_t stream);
+// Number of a sequence's first chunk. A sequence has a chunk more than its tokens fill, so that
+// the numbers of packed sequences follow from their offsets alone.
+__host__ __device__ inline int64_t gdr_chunk_base(const GdrArgs& a, int seq, int64_t first_token) {
+  return a.offsets == nullptr ? int64_t(seq) * ((a.T + kGdrChunk - 1) / kGdrChunk)
+                              : first_token / kGdrChunk + seq;
+}
 
 // Norm, gate, residual and next norm around a block (wkv_norm_gate.cu); null pointers are what
 // the entry points let a caller leave out.
