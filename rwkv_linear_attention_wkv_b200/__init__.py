@@ -16,7 +16,8 @@ __all__ = ["wkv_forward", "wkv_forward_bf16", "wkv_forward_state", "wkv_decode_s
            "wkv_backward", "wkv_backward_state", "wkv_backward_workspace_bytes",
            "wkv_forward_checkpointed", "wkv_backward_checkpointed",
            "wkv7_forward", "wkv_mstate_forward",
-           "wkv_gdr_forward", "wkv_gdr_decode_step",
+           "wkv_gdr_forward", "wkv_gdr_decode_step", "wkv_gdr_forward_checkpointed",
+           "wkv_gdr_backward",
            "wkv_norm_gate_forward", "wkv_norm_gate_backward", "wkv_norm_gate_workspace_bytes",
            "wkv_stream_status", "wkv_status_string", "WkvError", "lib",
            "LIB_PATH"]
@@ -57,6 +58,11 @@ _SIGS = {
     "wkv_testing_backward_timeout": ([ctypes.c_uint64, _P], ctypes.c_int),
     "wkv_testing_forward_plain": ([_I, _I, _I] + [_P] * 6 + [ctypes.c_int, _P], ctypes.c_int),
     "wkv_gdr_forward": ([_P] * 9 + [_P], ctypes.c_int),
+    "wkv_gdr_checkpoint_bytes": ([_P], ctypes.c_size_t),
+    "wkv_gdr_backward_workspace_bytes": ([_P], ctypes.c_size_t),
+    "wkv_gdr_forward_checkpointed": ([_P] * 10 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "wkv_gdr_backward": ([_P] * 7 + [ctypes.c_size_t] + [_P] * 8 + [ctypes.c_size_t, _P],
+                         ctypes.c_int),
     "wkv_gdr_decode_step": ([_P] * 8 + [_I, _P, _P], ctypes.c_int),
     "wkv_norm_gate_forward": ([_P] * 9 + [_P], ctypes.c_int),
     "wkv_norm_gate_workspace_bytes": ([_I, _I], ctypes.c_size_t),
@@ -448,6 +454,7 @@ def wkv_stream_status(stream=None) -> int:
 # Entry points whose binding is in a module of its own, which imports torch: loaded when first
 # used, so that importing the package (and loading the library) needs no torch.
 _IN_MODULES = {"wkv_gdr_forward": "gdr", "wkv_gdr_decode_step": "gdr",
+               "wkv_gdr_forward_checkpointed": "gdr", "wkv_gdr_backward": "gdr",
                "wkv_norm_gate_forward": "norm_gate", "wkv_norm_gate_backward": "norm_gate",
                "wkv_norm_gate_workspace_bytes": "norm_gate"}
 

@@ -30,6 +30,7 @@
 namespace wkv {
 namespace gdr {
 
+constexpr int kStagePitch = 24;  // bf16 staging of a warp's 16 x 16 outputs
 constexpr int kG = 16;  // tokens of a group: one k step of the matrix instruction
 
 // Below this a log-decay counts as a decay of zero: e^-200 is far below the smallest float.
@@ -44,6 +45,14 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
+}
+
+// Four 8 x 8 tiles of bf16 pairs, each stored transposed.
+__device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                       uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
 }
 
 // c (16 x 8) += a (16 x 16) b (16 x 8), bf16 with fp32 sums. Thread (g, t) = (lane / 4, lane % 4)
@@ -169,45 +178,349 @@ __device__ __forceinline__ int64_t sequence(const GdrArgs& a, int seq, int& len)
   return t0;
 }
 
-// Inclusive sums over the group's 16 tokens of g log2(e), in every lane for token lane % 16, in
-// fp64: decays between two tokens are differences of these, and a strong decay earlier in the
-// group must not cost the later ones their digits.
-__device__ __forceinline__ double decay_sums(float g, int lane) {
-  double s = double(g < kLeastG ? kLeastG : g) * 1.4426950408889634;
+// A running log2-decay as an unevaluated sum of two floats (48 bits): decays between two tokens
+// are differences of such sums, and a strong decay earlier must not cost later ones their digits.
+// (fp64 took 4 times as long here: its unit is slow and its shuffles come in pairs.)
+struct Decay {
+  float hi, lo;
+};
+__device__ __forceinline__ Decay add(Decay a, Decay b) {
+  const float s = __fadd_rn(a.hi, b.hi), v = __fsub_rn(s, a.hi);
+  const float err = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, v)), __fsub_rn(b.hi, v));
+  const float lo = err + (a.lo + b.lo);
+  const float hi = __fadd_rn(s, lo);
+  return {hi, __fsub_rn(lo, __fsub_rn(hi, s))};
+}
+// exp of the decay from one running sum to a later one.
+__device__ __forceinline__ float decay_between(Decay to, Decay from) {
+  return ex2((to.hi - from.hi) + (to.lo - from.lo));
+}
+__device__ __forceinline__ Decay shfl(Decay d, int lane) {
+  return {__shfl_sync(0xffffffffu, d.hi, lane), __shfl_sync(0xffffffffu, d.lo, lane)};
+}
+
+// Inclusive sums of g log2(e) over each WIDTH adjacent lanes.
+template <int WIDTH>
+__device__ __forceinline__ Decay decay_sums(float g, int lane) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  constexpr float kLog2eLo = float(1.4426950408889634 - double(kLog2e));
+  if (g < kLeastG) g = kLeastG;
+  Decay s;
+  s.hi = __fmul_rn(g, kLog2e);
+  s.lo = fmaf(g, kLog2eLo, fmaf(g, kLog2e, -s.hi));
 #pragma unroll
-  for (int d = 1; d < kG; d <<= 1) {
-    const double below = __shfl_up_sync(0xffffffffu, s, d, 16);
-    if ((lane & 15) >= d) s += below;
+  for (int d = 1; d < WIDTH; d <<= 1) {
+    const Decay below = {__shfl_up_sync(0xffffffffu, s.hi, d, WIDTH),
+                         __shfl_up_sync(0xffffffffu, s.lo, d, WIDTH)};
+    const Decay sum = add(s, below);
+    if ((lane & (WIDTH - 1)) >= d) s = sum;
   }
   return s;
 }
 
 // The strictly lower part of (I + L)^-1 for a strictly lower 16 x 16 L in shared memory (pitch
-// 20), by forward substitution, one column a lane; left in the same place.
+// 20), left in the same place. The two diagonal 8 x 8 blocks A and B by forward substitution,
+// one column a lane; the block below them is -B^-1 (L21 A^-1). `tmp`: 8 x 8 floats.
 constexpr int kLP = 20;
-__device__ __forceinline__ void invert_group(float* L, int lane) {
-  const int c = lane & 15;
-  float x[kG];
+constexpr int kLTmp = 64;
+__device__ __forceinline__ void invert_group(float* L, float* tmp, int lane) {
+  const int b = (lane >> 3) & 1, c = lane & 7;
+  const float* const D = L + b * 8 * (kLP + 1);
   __syncwarp();
+  float4 r[8][2];
 #pragma unroll
-  for (int i = 0; i < kG; ++i) {
+  for (int i = 1; i < 8; ++i) {
+    r[i][0] = *reinterpret_cast<const float4*>(D + i * kLP);
+    if (i > 4) r[i][1] = *reinterpret_cast<const float4*>(D + i * kLP + 4);
+  }
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float* l = reinterpret_cast<const float*>(r[i]);
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int j = 0; j < i; j += 4) {
-      const float4 l = *reinterpret_cast<const float4*>(L + i * kLP + j);
-      s0 = fmaf(l.x, x[j], s0);
-      if (j + 1 < i) s1 = fmaf(l.y, x[j + 1], s1);
-      if (j + 2 < i) s0 = fmaf(l.z, x[j + 2], s0);
-      if (j + 3 < i) s1 = fmaf(l.w, x[j + 3], s1);
-    }
+    for (int j = 0; j < i; ++j) (j & 1 ? s1 : s0) = fmaf(l[j], x[j], j & 1 ? s1 : s0);
     x[i] = i < c ? 0.f : i == c ? 1.f : -(s0 + s1);
   }
   __syncwarp();
-  if (lane < kG) {
+  // rows of A^-1 and B^-1 with their unit diagonals
+  if (lane < 16) {
 #pragma unroll
-    for (int i = 0; i < kG; ++i) L[i * kLP + c] = i == c ? 0.f : x[i];
+    for (int i = 0; i < 8; ++i) L[(b * 8 + i) * kLP + b * 8 + c] = x[i];
   }
   __syncwarp();
+  const int row = lane >> 2, col = (lane & 3) * 2;
+  {
+    const float4 l0 = *reinterpret_cast<const float4*>(L + (8 + row) * kLP);
+    const float4 l1 = *reinterpret_cast<const float4*>(L + (8 + row) * kLP + 4);
+    const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+    float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 y = *reinterpret_cast<const float2*>(L + k * kLP + col);
+      t0 = fmaf(l[k], y.x, t0);
+      t1 = fmaf(l[k], y.y, t1);
+    }
+    *reinterpret_cast<float2*>(tmp + row * 8 + col) = make_float2(t0, t1);
+  }
+  __syncwarp();
+  {
+    const float4 l0 = *reinterpret_cast<const float4*>(L + (8 + row) * kLP + 8);
+    const float4 l1 = *reinterpret_cast<const float4*>(L + (8 + row) * kLP + 12);
+    const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+    float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 y = *reinterpret_cast<const float2*>(tmp + k * 8 + col);
+      t0 = fmaf(l[k], y.x, t0);
+      t1 = fmaf(l[k], y.y, t1);
+    }
+    *reinterpret_cast<float2*>(L + (8 + row) * kLP + col) = make_float2(-t0, -t1);
+  }
+  if (lane < kG) L[lane * (kLP + 1)] = 0.f;
+  __syncwarp();
+}
+
+// One tensor's tile of a step: kStep rows of ROW bytes into rows PITCH bytes apart, 16 bytes a
+// copy, by THREADS threads. src: the step's first row; rows past `left` become zeros.
+template <int STEP, int ROW, int PITCH, int THREADS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const void* src, int64_t stride, int left,
+                                          int thread) {
+  constexpr int kChunks = ROW / 16, kAtOnce = THREADS / kChunks;
+  static_assert(THREADS % kChunks == 0 && STEP % kAtOnce == 0, "whole rows a pass");
+  const int t = thread / kChunks, c = thread % kChunks;
+  const char* p = static_cast<const char*>(src) + t * stride + c * 16;
+  dst += uint32_t(t * PITCH + c * 16);
+  if (left >= STEP) {
+#pragma unroll
+    for (int j = 0; j < STEP / kAtOnce; ++j)
+      cp_async_16z(dst + j * kAtOnce * PITCH, p + j * kAtOnce * stride, true);
+  } else {
+#pragma unroll 1
+    for (int j = 0; j < STEP / kAtOnce; ++j) {
+      const bool ok = t + j * kAtOnce < left;
+      cp_async_16z(dst + j * kAtOnce * PITCH, ok ? p + j * kAtOnce * stride : src, ok);
+    }
+  }
+}
+
+// A warp's 16 tokens x N of fp32 (pitch N + 4) into three bf16 parts (pitch N + 8, PART bytes
+// apart).
+template <int N, int PART>
+__device__ __forceinline__ void split_tokens(const float* src, unsigned char* dst, int lane) {
+#pragma unroll 8
+  for (int j = 0; j < kG * N / 128; ++j) {
+    const int at = j * 32 + lane, r = at / (N / 4), c = (at % (N / 4)) * 4;
+    const float4 x = *reinterpret_cast<const float4*>(src + r * (N + 4) + c);
+    uint2 p0, p1, p2;
+    split2(x.x, x.y, p0.x, p1.x, p2.x);
+    split2(x.z, x.w, p0.y, p1.y, p2.y);
+    unsigned char* d = dst + (r * (N + 8) + c) * 2;
+    *reinterpret_cast<uint2*>(d) = p0;
+    *reinterpret_cast<uint2*>(d + PART) = p1;
+    *reinterpret_cast<uint2*>(d + 2 * PART) = p2;
+  }
+}
+
+// What the producers hand over for a group of 16 tokens: operand fragments (three parts, a uint4
+// a lane) of an inverse less its diagonal and of a read matrix, and vectors over the tokens.
+struct GroupMats {
+  uint4 inv[3][32];
+  uint4 read[3][32];
+  float decay[kG];  // C_i
+  float out[kG];    // scale C_i
+  float write[kG];  // forward: exp(c_16 - c_j) beta_j; reverse: exp(c_16 - c_j)
+  float beta[kG];   // reverse only
+  float end;        // C
+  float pad[3];
+};
+
+// Sizes of the two kernels that walk sequences in groups: NG producer warps, each with a group
+// of a step, and NC consumer warps of 16 value channels each. "v" is whatever comes per value
+// head: v, or dy.
+
+template <typename T, int N, int NC, int NG>
+struct Shape {
+  static constexpr bool kBf16 = sizeof(T) == 2;
+  static constexpr int kParts = kBf16 ? 1 : 3;      // operand parts of q and k
+  static constexpr int kStep = NG * kG;             // tokens of a step
+  static constexpr int kPitch = N + 8;              // bf16 tiles (16-byte rows, no conflicts)
+  static constexpr int kPitchF = N + 4;             // fp32 tiles
+  static constexpr int kTile = kStep * kPitch * 2;  // bytes of a bf16 tile
+  static constexpr int kTileF = kStep * kPitchF * 4;
+  static constexpr int kVRows = 16 * NC;            // value channels of the CTA
+  static constexpr int kVPitch = kBf16 ? kVRows + 8 : kVRows + 4;
+  static constexpr int kVTile = kStep * kVPitch * int(sizeof(T));
+  // bf16: rings of three for q, k, v. fp32: q and k arrive in a ring of two and are split into
+  // two sets of parts; v in a ring of three.
+  static constexpr int kQK = kBf16 ? 3 * 2 * kTile : 2 * 2 * kTileF;
+  static constexpr int kSplit = kBf16 ? 0 : 2 * 2 * 3 * kTile;
+  static constexpr int kOffSplit = kQK;
+  static constexpr int kOffV = kOffSplit + kSplit;
+  static constexpr int kOffMats = kOffV + 3 * kVTile;
+  static constexpr int kOffL = kOffMats + 2 * NG * int(sizeof(GroupMats));
+  static constexpr int kOffY = kOffL + NG * (kG * kLP + kLTmp) * 4;
+  static constexpr int kSmem = kOffY + (kBf16 ? NC * kG * kStagePitch * 2 : 0);
+  static constexpr int kThreads = 32 * (NC + NG);
+};
+
+
+// q, k (rows of N) and v (rows of kVRows) of a step of the sequence, by the producers.
+template <typename T, int N, class X, int NG>
+__device__ __forceinline__ void load_step(uint32_t kd, uint32_t qd, uint32_t vd, const T* k,
+                                          const T* q, const T* v, int64_t qk_row, int64_t v_row,
+                                          int first, int len, int thread) {
+  constexpr int kSize = int(sizeof(T)), kPitch = X::kBf16 ? X::kPitch * 2 : X::kPitchF * 4;
+  const int left = len - first;
+  load_tile<X::kStep, N * kSize, kPitch, NG * 32>(kd, k + first * qk_row, qk_row * kSize, left,
+                                                  thread);
+  load_tile<X::kStep, N * kSize, kPitch, NG * 32>(qd, q + first * qk_row, qk_row * kSize, left,
+                                                  thread);
+  load_tile<X::kStep, X::kVRows * kSize, X::kVPitch * kSize, NG * 32>(
+      vd, v + first * v_row, v_row * kSize, left, thread);
+}
+
+// Two products over the channels of a group's tokens at byte offset `off` of every part's tile:
+// kk = K K^T, and Q K^T (or, Q_COLUMNS, K Q^T).
+template <int N, int P, bool Q_COLUMNS, class Tile>
+__device__ __forceinline__ void group_products(float (&kk)[2][4], float (&qk)[2][4], Tile tile,
+                                               uint32_t off) {
+  float kc[2][4], qc[2][4];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) zero(kk[n]), zero(qk[n]), zero(kc[n]), zero(qc[n]);
+#pragma unroll
+  for (int c = 0; c < N; c += 16) {
+    uint32_t kb[P][4], qb[P][4], ka[3][4], qa[3][4];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      ldsm4(kb[p], tile(0, p) + off + c * 2);
+      ldsm4(qb[p], tile(1, p) + off + c * 2);
+      // the same four 8 x 8 blocks in the order of an a operand
+      ka[p][0] = kb[p][0]; ka[p][1] = kb[p][2]; ka[p][2] = kb[p][1]; ka[p][3] = kb[p][3];
+      qa[p][0] = qb[p][0]; qa[p][1] = qb[p][2]; qa[p][2] = qb[p][1]; qa[p][3] = qb[p][3];
+    }
+    if constexpr (P == 1) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        mma(kk[n], ka[0], kb[0][2 * n], kb[0][2 * n + 1]);
+        if (Q_COLUMNS)
+          mma(qk[n], ka[0], qb[0][2 * n], qb[0][2 * n + 1]);
+        else
+          mma(qk[n], qa[0], kb[0][2 * n], kb[0][2 * n + 1]);
+      }
+    } else {
+      mma_pairs<P, true>(kk, kc, ka, kb);
+      if (Q_COLUMNS)
+        mma_pairs<P, true>(qk, qc, ka, qb);
+      else
+        mma_pairs<P, true>(qk, qc, qa, kb);
+    }
+  }
+  if (P > 1) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) kk[n][x] += kc[n][x], qk[n][x] += qc[n][x];
+  }
+}
+
+// Two pairs of adjacent accumulator tiles (rows: the product's columns) as the b operand of a
+// 16 x 16 product, PARTS parts of a uint4 a lane.
+template <int PARTS>
+__device__ __forceinline__ void put_fragment(uint4 (*to)[32], const float2& t00, const float2& t01,
+                                             const float2& t10, const float2& t11, int lane) {
+  uint4 f[3];
+  split2(t00.x, t00.y, f[0].x, f[1].x, f[2].x);
+  split2(t01.x, t01.y, f[0].y, f[1].y, f[2].y);
+  split2(t10.x, t10.y, f[0].z, f[1].z, f[2].z);
+  split2(t11.x, t11.y, f[0].w, f[1].w, f[2].w);
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) to[p][lane] = f[p];
+}
+
+// A warp's 16 channels x 16 tokens (accumulator tiles) to rows of tokens in global memory:
+// fp32 eight channels of a token at a time, bf16 through 16 x 24 elements of shared memory.
+template <typename T>
+__device__ __forceinline__ void put_tokens(T* to, int64_t row, const float (&x)[2][4], int left,
+                                           __nv_bfloat16* stage, int lane) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t r[2][2];  // token tile, channel half
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+        r[n][z] = bits(__float22bfloat162_rn(make_float2(x[n][2 * z], x[n][2 * z + 1])));
+    __syncwarp();
+    // tile m of the four: tokens 8 (m / 2).., channels 8 (m % 2)..
+    stsm4t(smem_u32(stage) + uint32_t(((lane >> 4) * 8 + (lane & 7)) * kStagePitch +
+                                      ((lane >> 3) & 1) * 8) * 2u,
+           r[0][0], r[0][1], r[1][0], r[1][1]);
+    __syncwarp();
+    const int tok = lane >> 1, c = (lane & 1) * 8;
+    if (tok < left)
+      *reinterpret_cast<uint4*>(to + tok * row + c) =
+          *reinterpret_cast<const uint4*>(stage + tok * kStagePitch + c);
+  } else {
+    const int g4 = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int tok = n * 8 + 2 * t4 + y;
+        if (tok < left) {
+          to[tok * row + g4] = x[n][y];
+          to[tok * row + g4 + 8] = x[n][2 + y];
+        }
+      }
+  }
+}
+
+// 16 channels x 16 tokens of v (or dy) as accumulator values; for bf16 also the raw operand.
+template <typename T, class X>
+__device__ __forceinline__ void get_tokens(float (&vv)[2][4], uint32_t (&raw)[4],
+                                           const unsigned char* tile, int token, int channel,
+                                           int lane) {
+  if constexpr (sizeof(T) == 2) {
+    ldsm4t(raw, smem_u32(tile) + uint32_t(token * X::kVPitch + channel) * 2u +
+                    at_transposed(lane, X::kVPitch));
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const float2 lo = unpack(raw[2 * n]), hi = unpack(raw[2 * n + 1]);
+      vv[n][0] = lo.x; vv[n][1] = lo.y; vv[n][2] = hi.x; vv[n][3] = hi.y;
+    }
+  } else {
+    const float* vp = reinterpret_cast<const float*>(tile) + token * X::kVPitch + channel;
+    const int g4 = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        vv[n][x] = vp[(n * 8 + 2 * t4 + (x & 1)) * X::kVPitch + g4 + (x >> 1) * 8];
+  }
+}
+
+// A warp's 16 rows x N of a state, as accumulator tiles, from and to global memory.
+template <int N>
+__device__ __forceinline__ void get_state(float (&S)[N / 8][4], const float* from, int lane) {
+  const int g4 = lane >> 2, t4 = lane & 3;
+#pragma unroll
+  for (int n = 0; n < N / 8; ++n) {
+    zero(S[n]);
+    if (from != nullptr) {
+      const float2 x = *reinterpret_cast<const float2*>(from + g4 * N + n * 8 + 2 * t4);
+      const float2 z = *reinterpret_cast<const float2*>(from + (g4 + 8) * N + n * 8 + 2 * t4);
+      S[n][0] = x.x; S[n][1] = x.y; S[n][2] = z.x; S[n][3] = z.y;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void put_state(float* to, const float (&S)[N / 8][4], int lane) {
+  const int g4 = lane >> 2, t4 = lane & 3;
+#pragma unroll
+  for (int n = 0; n < N / 8; ++n) {
+    *reinterpret_cast<float2*>(to + g4 * N + n * 8 + 2 * t4) = make_float2(S[n][0], S[n][1]);
+    *reinterpret_cast<float2*>(to + (g4 + 8) * N + n * 8 + 2 * t4) = make_float2(S[n][2], S[n][3]);
+  }
 }
 
 }  // namespace gdr

@@ -53,6 +53,41 @@ int pass_state(const float* s0, float* s1, size_t bytes, cudaStream_t stream) {
   return e == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
 }
 
+// Checkpoints: every token's e, then the state entering every chunk. Workspace: the same shapes.
+struct Saved {
+  size_t tokens, states;  // floats
+};
+Saved saved_of(const GdrArgs& a) {
+  return {size_t(a.B) * a.T * a.H * a.N, size_t(gdr_chunks(a)) * a.H * a.N * a.N};
+}
+size_t saved_bytes(const wkv_gdr_problem* p) {
+  bool empty;
+  if (check_problem(p, &empty) != WKV_OK || empty || p->T == 0) return 0;
+  const Saved s = saved_of(args_of(p));
+  return (s.tokens + s.states) * sizeof(float);
+}
+
+// Forward, with somewhere to put the checkpoints or without.
+int forward(const wkv_gdr_problem* p, const void* q, const void* k, const void* v, const float* g,
+            const float* beta, void* y, const float* s0, float* s1, bool keep, void* saved,
+            size_t saved_size, cudaStream_t stream) {
+  bool empty;
+  if (int rc = check_problem(p, &empty)) return rc;
+  if (empty) return WKV_OK;
+  if (p->T > 0 && (!q || !k || !v || !g || !beta || !y)) return WKV_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, (const void*)y, (const void*)s0, (const void*)s1,
+                        (const void*)saved})
+    if (!aligned(x, 16)) return WKV_ERR_ALIGNMENT;
+  if (!aligned(g, 4) || !aligned(beta, 4)) return WKV_ERR_ALIGNMENT;
+  GdrArgs a = args_of(p);
+  if (a.T == 0) return pass_state(s0, s1, size_t(a.n_seqs) * a.H * a.N * a.N * 4, stream);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.y = y; a.s0 = s0; a.s1 = s1;
+  if (!keep) return launch_gdr_chunked(a, nullptr, nullptr, stream);
+  if (saved == nullptr || saved_size < saved_bytes(p)) return WKV_ERR_INVALID_ARG;
+  float* e = static_cast<float*>(saved);
+  return launch_gdr_chunked(a, e, e + saved_of(a).tokens, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -60,17 +95,55 @@ extern "C" {
 WKV_API int wkv_gdr_forward(const wkv_gdr_problem* p, const void* q, const void* k,
                             const void* v, const float* g, const float* beta, void* y,
                             const float* s0, float* s1, cudaStream_t stream) {
+  return forward(p, q, k, v, g, beta, y, s0, s1, false, nullptr, 0, stream);
+}
+
+WKV_API size_t wkv_gdr_checkpoint_bytes(const wkv_gdr_problem* p) { return saved_bytes(p); }
+WKV_API size_t wkv_gdr_backward_workspace_bytes(const wkv_gdr_problem* p) {
+  return saved_bytes(p);
+}
+
+WKV_API int wkv_gdr_forward_checkpointed(const wkv_gdr_problem* p, const void* q, const void* k,
+                                         const void* v, const float* g, const float* beta, void* y,
+                                         const float* s0, float* s1, void* checkpoints,
+                                         size_t checkpoint_bytes, cudaStream_t stream) {
+  return forward(p, q, k, v, g, beta, y, s0, s1, true, checkpoints, checkpoint_bytes, stream);
+}
+
+WKV_API int wkv_gdr_backward(const wkv_gdr_problem* p, const void* q, const void* k,
+                             const float* g, const float* beta, const void* dy,
+                             const void* checkpoints, size_t checkpoint_bytes, const float* ds1,
+                             void* dq, void* dk, void* dv, float* dg, float* dbeta, float* ds0,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   bool empty;
   if (int rc = check_problem(p, &empty)) return rc;
   if (empty) return WKV_OK;
-  if (p->T > 0 && (!q || !k || !v || !g || !beta || !y)) return WKV_ERR_INVALID_ARG;
-  for (const void* x : {q, k, v, (const void*)y, (const void*)s0, (const void*)s1})
+  for (const void* x : {q, k, dy, checkpoints, (const void*)dq, (const void*)dk, (const void*)dv,
+                        (const void*)ds1, (const void*)ds0, (const void*)workspace})
     if (!aligned(x, 16)) return WKV_ERR_ALIGNMENT;
-  if (!aligned(g, 4) || !aligned(beta, 4)) return WKV_ERR_ALIGNMENT;
-  GdrArgs a = args_of(p);
-  if (a.T == 0) return pass_state(s0, s1, size_t(a.n_seqs) * a.H * a.N * a.N * 4, stream);
-  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.y = y; a.s0 = s0; a.s1 = s1;
-  return launch_gdr_chunked(a, nullptr, nullptr, stream);
+  for (const void* x : {(const void*)g, (const void*)beta, (const void*)dg, (const void*)dbeta})
+    if (!aligned(x, 4)) return WKV_ERR_ALIGNMENT;
+  GdrBwdArgs b{};
+  b.p = args_of(p);
+  if (p->T == 0)
+    return pass_state(ds1, ds0, size_t(b.p.n_seqs) * b.p.H * b.p.N * b.p.N * 4, stream);
+  for (const void* x : {q, k, (const void*)g, (const void*)beta, dy, checkpoints, (const void*)dq,
+                        (const void*)dk, (const void*)dv, (const void*)dg, (const void*)dbeta,
+                        (const void*)workspace})
+    if (x == nullptr) return WKV_ERR_INVALID_ARG;
+  if (checkpoint_bytes < saved_bytes(p) || workspace_bytes < saved_bytes(p))
+    return WKV_ERR_INVALID_ARG;
+  if (gdr_chunks(b.p) > ((int64_t(1) << 31) - 1) / b.p.Hk) return WKV_ERR_UNSUPPORTED;
+  const Saved s = saved_of(b.p);
+  b.p.q = q; b.p.k = k; b.p.g = g; b.p.beta = beta;
+  b.dy = dy;
+  b.e = static_cast<const float*>(checkpoints);
+  b.checkpoints = b.e + s.tokens;
+  b.ds1 = ds1;
+  b.du = static_cast<float*>(workspace);
+  b.dstates = b.du + s.tokens;
+  b.dq = dq; b.dk = dk; b.dv = dv; b.dg = dg; b.dbeta = dbeta; b.ds0 = ds0;
+  return launch_gdr_backward(b, stream);
 }
 
 WKV_API int wkv_gdr_decode_step(const wkv_gdr_problem* p, const void* q, const void* k,

@@ -1,0 +1,741 @@
+// Gradients of the gated delta rule (sm_100a), in two kernels.
+//
+// With u_j = beta_j e_j what a token writes, D the gradient of the state after it, and per group
+// of 16 tokens c_i, D_ij, C_i, C as in the forward, dD the gradient of the state that leaves:
+//   R_j  = exp(c_16 - c_j) dD k_j + scale sum_{i >= j} D_ij (q_i . k_j) dy_i
+//   du_j = R_j - sum_{i > j} D_ij (k_i . k_j) beta_i du_i,     de = beta du = dv
+//   dD  <- C dD + sum_i (scale C_i dy_i) q_i^T - (C_i de_i) k_i^T
+// 1. The chain walks a sequence's groups from the last to the first. It is the forward with dy in
+//    the place of v: rows of dD (value channels) stay in registers, 16 a warp, the system is the
+//    forward's transposed. It leaves du, and dD after every chunk of 64 tokens.
+// 2. Everything else needs sums over value channels, but no chain: a CTA takes a chunk of one
+//    query/key head, with the state S that enters it (the forward's checkpoint), the gradient dD
+//    of the one that leaves, e and du, and per value head
+//      P_ij = scale D_ij (dy_i . u_j) (i >= j),   Z_ij = D_ij (de_i . u_j) (i > j)
+//      dq = scale C S^T dy + P K
+//      dk = [exp(c_L - c) dD^T u + P^T Q - Z^T K] + [-C S^T de - Z K]
+//      dbeta_j = du_j . e_j
+//      dg_t = <dD, S_L> + sum_{i >= t} q_i . dq_i + k_i . [second] - k_i . [first],
+//    since c_i enters with a plus where token i reads and a minus where it writes.
+//
+// Rounding: the chain keeps the full three-part products everywhere (its results feed fp32
+// gradients of states). In the second kernel bf16 problems take two parts (2^-17 a factor), well
+// below the bf16 rounding of dq and dk; fp32 problems take three.
+#include <algorithm>
+
+#include "wkv_gdr.cuh"
+
+namespace wkv {
+
+using namespace gdr;
+
+namespace {
+
+// c += a b with a of one exact part and b of three, the small products first.
+__device__ __forceinline__ void mma_exact_a(float (&c)[2][4], const uint32_t (&a)[4],
+                                            const uint32_t (&b)[3][4]) {
+#pragma unroll
+  for (int p = 2; p >= 0; --p)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) mma(c[n], a, b[p][2 * n], b[p][2 * n + 1]);
+}
+
+template <typename T, int N, int NC, int NG, int CTAS>
+__global__ void __launch_bounds__(Shape<T, N, NC, NG>::kThreads, CTAS)
+    gdr_chain_kernel(GdrBwdArgs b) {
+  using X = Shape<T, N, NC, NG>;
+  constexpr int P = X::kParts;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const GdrArgs& a = b.p;
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g4 = lane >> 2, t4 = lane & 3;
+  constexpr int kSplitRows = N / X::kVRows;
+  const int part = blockIdx.x % kSplitRows;
+  const int sh = blockIdx.x / kSplitRows;
+  const int seq = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
+  int len;
+  const int64_t t0 = sequence(a, seq, len);
+  const int steps = (len + X::kStep - 1) / X::kStep;
+  GroupMats* const mats = reinterpret_cast<GroupMats*>(smem + X::kOffMats);  // [2][NG]
+  const int64_t qk_row = int64_t(a.Hk) * N, v_row = int64_t(a.H) * N;
+
+  // Steps are counted in the order they are taken: step i has the tokens from `first_of(i)`.
+  auto first_of = [&](int i) { return (steps - 1 - i) * X::kStep; };
+  auto tile = [&](int s, int which, int p) -> uint32_t {
+    if (X::kBf16) return sb + ((s % 3) * 2 + which) * X::kTile;
+    return sb + X::kOffSplit + (((s & 1) * 2 + which) * 3 + p) * X::kTile;
+  };
+
+  if (warp >= NC) {
+    // ------------------------------------------------------------------ producers
+    const int pw = warp - NC, pt = pw * 32 + lane;
+    const T* q = static_cast<const T*>(a.q) + t0 * qk_row + int64_t(hk) * N;
+    const T* k = static_cast<const T*>(a.k) + t0 * qk_row + int64_t(hk) * N;
+    const T* dy = static_cast<const T*>(b.dy) + t0 * v_row + int64_t(h) * N + part * X::kVRows;
+    const float* gp = a.g + t0 * a.H + h;
+    const float* bp = a.beta + t0 * a.H + h;
+    float* const L = reinterpret_cast<float*>(smem + X::kOffL) + pw * kG * kLP;
+    float* const tmp = reinterpret_cast<float*>(smem + X::kOffL) + NG * kG * kLP + pw * kLTmp;
+
+    auto load = [&](int s) {
+      if (s < steps)
+        load_step<T, N, X, NG>(X::kBf16 ? tile(s, 0, 0) : sb + ((s & 1) * 2 + 0) * X::kTileF,
+                               X::kBf16 ? tile(s, 1, 0) : sb + ((s & 1) * 2 + 1) * X::kTileF,
+                               sb + X::kOffV + (s % 3) * X::kVTile, k, q, dy, qk_row, v_row,
+                               first_of(s), len, pt);
+      cp_async_commit();
+    };
+    float g_next = 0.f, b_next = 0.f;
+    auto load_g = [&](int s) {
+      const int tok = first_of(s) + pw * kG + (lane & 15);
+      const bool ok = s < steps && tok < len;
+      g_next = ok ? gp[int64_t(tok) * a.H] : 0.f;
+      b_next = ok ? bp[int64_t(tok) * a.H] : 0.f;
+    };
+    auto sync_producers = [&] {
+      if (NG == 1)
+        __syncwarp();
+      else
+        asm volatile("bar.sync 1, %0;" ::"n"(NG * 32) : "memory");
+    };
+
+    load(0);
+    load_g(0);
+    load(1);
+    for (int i = -1; i < steps; ++i) {
+      const int s = i + 1;  // the step to prepare
+      if (i >= 0) load(i + 2);
+      if (s < steps) {
+        const float gv = g_next, bv = b_next;
+        load_g(s + 1);
+        cp_async_wait<1>();
+        sync_producers();
+        if (!X::kBf16) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            split_tokens<N, X::kTile>(
+                reinterpret_cast<const float*>(smem + ((s & 1) * 2 + w) * X::kTileF) +
+                    pw * kG * X::kPitchF,
+                smem + (tile(s, w, 0) - sb) + pw * kG * X::kPitch * 2, lane);
+          __syncwarp();
+        }
+        // k_i . k_j (rows i) and k_j . q_i (rows j)
+        float kk[2][4], kq[2][4];
+        group_products<N, P, true>(
+            kk, kq, [&](int w, int p) { return tile(s, w, p); },
+            at_tokens(lane, X::kPitch) + uint32_t(pw * kG * X::kPitch) * 2u);
+        const Decay cs = decay_sums<kG>(gv, lane);
+        GroupMats& m = mats[(s & 1) * NG + pw];
+        float read[2][4];
+        const Decay cr[2] = {shfl(cs, g4), shfl(cs, g4 + 8)};
+        const float br[2] = {__shfl_sync(0xffffffffu, bv, g4),
+                             __shfl_sync(0xffffffffu, bv, g4 + 8)};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int col = n * 8 + 2 * t4 + y;
+            const Decay cc = shfl(cs, col);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int row = g4 + z * 8, x = 2 * z + y;
+              L[row * kLP + col] =
+                  row > col ? decay_between(cr[z], cc) * br[z] * kk[n][x] : 0.f;
+              read[n][x] = col >= row ? a.scale * (decay_between(cc, cr[z]) * kq[n][x]) : 0.f;
+            }
+          }
+        auto two = [](const float(&t)[4], int i) { return make_float2(t[i], t[i + 1]); };
+        put_fragment<3>(m.read, two(read[0], 0), two(read[1], 0), two(read[0], 2), two(read[1], 2),
+                        lane);
+        invert_group(L, tmp, lane);
+        // the transposed inverse: entry (i, j) multiplies R_i into du_j
+        auto down = [&](int i, int j) {
+          return make_float2(L[i * kLP + j], L[(i + 1) * kLP + j]);
+        };
+        put_fragment<3>(m.inv, down(2 * t4, g4), down(8 + 2 * t4, g4), down(2 * t4, g4 + 8),
+                        down(8 + 2 * t4, g4 + 8), lane);
+        const Decay last = shfl(cs, 15);
+        if (lane < kG) {
+          const float d = ex2(cs.hi + cs.lo);
+          m.decay[lane] = d;
+          m.out[lane] = a.scale * d;
+          m.write[lane] = decay_between(last, cs);
+          m.beta[lane] = bv;
+          if (lane == 15) m.end = d;
+        }
+      }
+      __syncthreads();
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------------- consumers
+  const int r0 = part * X::kVRows + warp * 16;  // this warp's value channels
+  const int64_t state_at = ((int64_t(seq) * a.H + h) * N + r0) * N;
+  float S[N / 8][4];  // dD: 16 rows x N columns
+  get_state<N>(S, b.ds1 == nullptr ? nullptr : b.ds1 + state_at, lane);
+  T* dv = static_cast<T*>(b.dv) + t0 * v_row + int64_t(h) * N + r0;
+  float* du = b.du + t0 * v_row + int64_t(h) * N + r0;
+  __nv_bfloat16* const stage =
+      reinterpret_cast<__nv_bfloat16*>(smem + X::kOffY) + warp * kG * kStagePitch;
+  constexpr int kChunk = gdr_chunk(X::kBf16, N);
+  float* const dstates = b.dstates + gdr_chunk_base(a, seq, t0) * a.H * N * N +
+                         (int64_t(h) * N + r0) * N;
+
+  __syncthreads();  // the first step is prepared
+  for (int i = 0; i < steps; ++i) {
+#pragma unroll 1
+    for (int gi = NG - 1; gi >= 0; --gi) {
+      const int first = first_of(i) + gi * kG;
+      if (first >= len) continue;
+      if ((first + kG) % kChunk == 0 || first + kG >= len)
+        put_state<N>(dstates + int64_t(first / kChunk) * a.H * N * N, S, lane);
+      const GroupMats& m = mats[(i & 1) * NG + gi];
+      const uint32_t grp = uint32_t(gi * kG * X::kPitch) * 2u;
+      // dD K^T
+      float xm[2][4], xc[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) zero(xm[n]), zero(xc[n]);
+      const uint32_t to = at_tokens(lane, X::kPitch) + grp;
+#pragma unroll
+      for (int c = 0; c < N; c += 16) {
+        uint32_t sp[3][4], kb[P][4];
+#pragma unroll
+        for (int p = 0; p < P; ++p) ldsm4(kb[p], tile(i, 0, p) + to + c * 2);
+        split_tiles(S[c / 8], S[c / 8 + 1], sp);
+        mma_pairs<P, true>(xm, xc, sp, kb);
+      }
+      // R^T
+      float vv[2][4], r[2][4];
+      uint32_t raw[4], ap[3][4], fb[3][4];
+      get_tokens<T, X>(vv, raw, smem + X::kOffV + (i % 3) * X::kVTile, gi * kG, warp * 16, lane);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(fb[p]) = m.read[p][lane];
+      zero(r[0]);
+      zero(r[1]);
+      if constexpr (X::kBf16) {
+        mma_exact_a(r, raw, fb);
+      } else {
+        split_tiles(vv[0], vv[1], ap);
+        mma_up<3, true>(r, ap, fb);
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float2 w = *reinterpret_cast<const float2*>(m.write + n * 8 + 2 * t4);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          r[n][x] = fmaf((x & 1) ? w.y : w.x, xm[n][x] + xc[n][x], r[n][x]);
+      }
+      // du^T = R^T (inverse)^T
+      split_tiles(r[0], r[1], ap);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(fb[p]) = m.inv[p][lane];
+      float ec[2][4];
+      zero(ec[0]);
+      zero(ec[1]);
+      mma_up<3, true>(ec, ap, fb);
+      float de[2][4], w1[2][4], w2[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float2 be = *reinterpret_cast<const float2*>(m.beta + n * 8 + 2 * t4);
+        const float2 dc = *reinterpret_cast<const float2*>(m.decay + n * 8 + 2 * t4);
+        const float2 ou = *reinterpret_cast<const float2*>(m.out + n * 8 + 2 * t4);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          r[n][x] += ec[n][x];
+          de[n][x] = r[n][x] * ((x & 1) ? be.y : be.x);
+          w1[n][x] = vv[n][x] * ((x & 1) ? ou.y : ou.x);
+          w2[n][x] = -de[n][x] * ((x & 1) ? dc.y : dc.x);
+        }
+      }
+      // dD = C dD + W1^T Q + W2^T K
+      uint32_t bp[3][4];
+      split_tiles(w1[0], w1[1], ap);
+      split_tiles(w2[0], w2[1], bp);
+      const float end = m.end;
+      const uint32_t ch = at_channels(lane, X::kPitch) + grp;
+#pragma unroll
+      for (int c = 0; c < N; c += 16) {
+        uint32_t kb[P][4], qb[P][4];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          ldsm4t(kb[p], tile(i, 0, p) + ch + c * 2);
+          ldsm4t(qb[p], tile(i, 1, p) + ch + c * 2);
+        }
+        float d[2][4];
+        zero(d[0]);
+        zero(d[1]);
+        mma_up<P, true>(d, ap, qb);
+        mma_up<P, true>(d, bp, kb);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) S[c / 8 + n][x] = fmaf(end, S[c / 8 + n][x], d[n][x]);
+      }
+      put_tokens<float>(du + first * v_row, v_row, r, len - first, nullptr, lane);
+      put_tokens<T>(dv + first * v_row, v_row, de, len - first, stage, lane);
+    }
+    __syncthreads();
+  }
+  if (b.ds0 != nullptr) put_state<N>(b.ds0 + state_at, S, lane);
+}
+
+// ---- the second kernel ----------------------------------------------------------------------
+
+template <typename T, int N>
+struct Chunk {
+  static constexpr bool kBf16 = sizeof(T) == 2;
+  static constexpr int kLen = gdr_chunk(kBf16, N);    // tokens
+  static constexpr int kIn = kBf16 ? 1 : 3;           // parts of q, k, dy
+  static constexpr int kParts = kBf16 ? 2 : 3;        // parts of u, de, states, P, Z
+  static constexpr int kCols = N == 64 ? 64 : kBf16 ? 64 : 32;  // columns of a warp
+  static constexpr int kSlices = N / kCols;           // warps that share a strip of 16 tokens
+  static constexpr int kWarps = kLen / 16 * kSlices;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kPitch = N + 8;
+  static constexpr int kTile = kLen * kPitch * 2;
+  static constexpr int kRows = 64;                    // rows of a state staged at once
+  static constexpr int kState = kRows * kPitch * 2;
+  static constexpr int kPPitch = kLen + 8;
+  static constexpr int kPTile = kLen * kPPitch * 2;
+  static constexpr int kOffK = 0;
+  static constexpr int kOffQ = kOffK + kIn * kTile;
+  static constexpr int kOffDy = kOffQ + kIn * kTile;
+  static constexpr int kOffU = kOffDy + kIn * kTile;
+  static constexpr int kOffDe = kOffU + kParts * kTile;
+  // a state's rows; later P in the same place
+  static constexpr int kOffS = kOffDe + kParts * kTile;
+  static constexpr int kOffZ = kOffS + kParts * (kState > kPTile ? kState : kPTile);
+  static constexpr int kOffF = kOffZ + kParts * kPTile;  // floats, see Floats
+  struct Floats {
+    Decay c[kLen];
+    float beta[kLen];
+    float to_end[kLen];      // exp(c_L - c_j)
+    float since[kLen];       // C_i
+    float dots[3][kSlices][kLen];
+    float inner[kWarps];     // <dD, S> by warp
+  };
+  static constexpr int kSmem = kOffF + int(sizeof(Floats));
+};
+
+// One value as PARTS bf16 parts, four at a time, PART bytes apart.
+template <int PARTS, int PART>
+__device__ __forceinline__ void put_parts(unsigned char* d, float4 x) {
+  uint2 p[3];
+  split2(x.x, x.y, p[0].x, p[1].x, p[2].x);
+  split2(x.z, x.w, p[0].y, p[1].y, p[2].y);
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) *reinterpret_cast<uint2*>(d + i * PART) = p[i];
+}
+
+// Products of operands of PA and PB parts: what a factor's parts leave out, the pairs do too.
+template <int PA, int PB, int NT>
+__device__ __forceinline__ void mma_parts(float (&c)[NT][4], int n, const uint32_t (&a)[PA][4],
+                                          const uint32_t (&b)[PB][4]) {
+  constexpr int kMost = PA > PB ? PA : PB;
+#pragma unroll
+  for (int sum = kMost - 1; sum >= 0; --sum)
+#pragma unroll
+    for (int i = PA - 1; i >= 0; --i) {
+      const int j = sum - i;
+      if (j < 0 || j >= PB) continue;
+      mma(c[n], a[i], b[j][0], b[j][1]);
+      mma(c[n + 1], a[i], b[j][2], b[j][3]);
+    }
+}
+
+// c (16 rows x 8 NT columns) += A B over LEN: A's fragments at `a` + 32 bytes a step, B's rows at
+// `b` + 16 rows a step, columns 32 bytes apart a tile pair. TA: A stored transposed.
+template <int PA, int PB, int NT, int LEN, bool TA, bool TB>
+__device__ __forceinline__ void product(float (&c)[NT][4], uint32_t a, int a_part, int a_pitch,
+                                        uint32_t b, int b_part, int b_pitch) {
+#pragma unroll 2
+  for (int l = 0; l < LEN; l += 16) {
+    uint32_t ap[PA][4];
+#pragma unroll
+    for (int p = 0; p < PA; ++p) {
+      if (TA)
+        ldsm4t(ap[p], a + p * a_part + l * a_pitch * 2);
+      else
+        ldsm4(ap[p], a + p * a_part + l * 2);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      uint32_t bp[PB][4];
+#pragma unroll
+      for (int p = 0; p < PB; ++p) {
+        if (TB)  // rows are the contraction
+          ldsm4t(bp[p], b + p * b_part + l * b_pitch * 2 + n * 16);
+        else     // rows are the product's columns
+          ldsm4(bp[p], b + p * b_part + n * 8 * b_pitch * 2 + l * 2);
+      }
+      mma_parts<PA, PB, NT>(c, n, ap, bp);
+    }
+  }
+}
+
+// a operand of 16 rows x 16 columns stored by rows (plain load) or by columns (transposed load).
+__device__ __forceinline__ uint32_t at_rows(int lane, int pitch) {
+  const int m = lane >> 3, r = lane & 7;
+  return uint32_t(((m & 1) * 8 + r) * pitch + (m >> 1) * 8) * 2u;
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(Chunk<T, N>::kThreads)
+    gdr_chunk_kernel(GdrBwdArgs b) {
+  using X = Chunk<T, N>;
+  constexpr int PI = X::kIn, PP = X::kParts, NT = X::kCols / 8, L = X::kLen;
+  extern __shared__ __align__(128) unsigned char smem[];
+  typename X::Floats& F = *reinterpret_cast<typename X::Floats*>(smem + X::kOffF);
+  const GdrArgs& a = b.p;
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g4 = lane >> 2, t4 = lane & 3;
+  const int strip = warp / X::kSlices, slice = warp % X::kSlices;
+  const int G = a.H / a.Hk;
+  const int hk = blockIdx.x % a.Hk;
+  const int64_t slot = blockIdx.x / a.Hk;
+  // the sequence and chunk of this slot
+  int seq = -1, chunk = 0, len = 0;
+  int64_t t0 = 0;
+  if (a.offsets == nullptr) {
+    const int per = (a.T + L - 1) / L;
+    seq = int(slot / per);
+    chunk = int(slot % per);
+    t0 = sequence(a, seq, len);
+  } else {
+    for (int s0 = 0; s0 < a.n_seqs && seq < 0; s0 += 32) {
+      bool mine = false;
+      if (s0 + lane < a.n_seqs) {
+        const int64_t first = sequence(a, s0 + lane, len);
+        const int64_t at = slot - gdr_chunk_base(a, s0 + lane, first);
+        mine = at >= 0 && at * L < len;
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, mine);
+      if (who != 0) seq = s0 + __ffs(who) - 1;
+    }
+    if (seq < 0) return;
+    t0 = sequence(a, seq, len);
+    chunk = int(slot - gdr_chunk_base(a, seq, t0));
+  }
+  t0 += int64_t(chunk) * L;
+  len = min(len - chunk * L, L);
+  const int64_t qk_row = int64_t(a.Hk) * N, v_row = int64_t(a.H) * N;
+  constexpr int kQuads = N / 4;
+
+  // the chunk's rows of an input into PI parts, zeros past `len`
+  auto load_input = [&](const T* src, int64_t row, int off) {
+    if constexpr (X::kBf16) {
+      for (int i = threadIdx.x; i < L * (N / 8); i += X::kThreads) {
+        const int t = i / (N / 8), c = (i % (N / 8)) * 8;
+        const bool ok = t < len;
+        cp_async_16z(sb + off + uint32_t(t * X::kPitch + c) * 2u, src + (ok ? t : 0) * row + c, ok);
+      }
+    } else {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < L * kQuads; i += X::kThreads) {
+        const int t = i / kQuads, c = (i % kQuads) * 4;
+        const float4 x = t < len ? *reinterpret_cast<const float4*>(src + t * row + c)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        put_parts<3, X::kTile>(smem + off + (t * X::kPitch + c) * 2, x);
+      }
+    }
+  };
+  load_input(static_cast<const T*>(a.k) + t0 * qk_row + int64_t(hk) * N, qk_row, X::kOffK);
+  load_input(static_cast<const T*>(a.q) + t0 * qk_row + int64_t(hk) * N, qk_row, X::kOffQ);
+
+  // sum over this thread's columns of x times an input's rows, for its two tokens, left in F.dots
+  auto dot_rows = [&](const float(&x)[NT][4], int off, float(&out)[2]) {
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const unsigned char* r = smem + off + ((strip * 16 + g4 + z * 8) * X::kPitch +
+                                             slice * X::kCols + 2 * t4) * 2;
+      float s = 0.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int p = PI - 1; p >= 0; --p) {
+          const float2 w = unpack(*reinterpret_cast<const uint32_t*>(r + p * X::kTile + n * 16));
+          v.x += w.x;
+          v.y += w.y;
+        }
+        s = fmaf(x[n][2 * z], v.x, s);
+        s = fmaf(x[n][2 * z + 1], v.y, s);
+      }
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      out[z] = s;
+    }
+  };
+
+  float dq[NT][4], dk[NT][4];  // sums over the value heads
+#pragma unroll
+  for (int n = 0; n < NT; ++n) zero(dq[n]), zero(dk[n]);
+
+#pragma unroll 1
+  for (int h = hk * G; h < hk * G + G; ++h) {
+    const int64_t state_at = (slot * a.H + h) * N * N;
+    __syncthreads();  // the last head's tiles have been read
+    load_input(static_cast<const T*>(b.dy) + t0 * v_row + int64_t(h) * N, v_row, X::kOffDy);
+    if (threadIdx.x < 32) {
+      // decays over the chunk, L / 32 adjacent stretches of 32 tokens
+      Decay carry = {0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < L; s += 32) {
+        const int t = s + lane;
+        const float g = t < len ? a.g[(t0 + t) * a.H + h] : 0.f;
+        const Decay c = add(decay_sums<32>(g, lane), carry);
+        F.c[t] = c;
+        F.since[t] = ex2(c.hi + c.lo);
+        carry = shfl(c, 31);
+      }
+#pragma unroll
+      for (int s = 0; s < L; s += 32) F.to_end[s + lane] = decay_between(carry, F.c[s + lane]);
+    } else if (threadIdx.x < 32 + L) {
+      const int t = threadIdx.x - 32;
+      F.beta[t] = t < len ? a.beta[(t0 + t) * a.H + h] : 0.f;
+    }
+    __syncthreads();
+    // u, de, dbeta: a token's row lies in kQuads adjacent lanes
+#pragma unroll 4
+    for (int i = threadIdx.x; i < L * kQuads; i += X::kThreads) {
+      const int t = i / kQuads, c = (i % kQuads) * 4;
+      float4 e = make_float4(0.f, 0.f, 0.f, 0.f), d = e;
+      const int64_t at = (t0 + t) * v_row + int64_t(h) * N + c;
+      if (t < len) {
+        e = *reinterpret_cast<const float4*>(b.e + at);
+        d = *reinterpret_cast<const float4*>(b.du + at);
+      }
+      const float be = F.beta[t];
+      float s = fmaf(e.x, d.x, fmaf(e.y, d.y, fmaf(e.z, d.z, e.w * d.w)));
+#pragma unroll
+      for (int m = kQuads / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+      if (c == 0 && t < len) b.dbeta[(t0 + t) * a.H + h] = s;
+      const int to = (t * X::kPitch + c) * 2;
+      put_parts<PP, X::kTile>(smem + X::kOffU + to,
+                              make_float4(be * e.x, be * e.y, be * e.z, be * e.w));
+      put_parts<PP, X::kTile>(smem + X::kOffDe + to,
+                              make_float4(be * d.x, be * d.y, be * d.z, be * d.w));
+    }
+    // 64 rows of a state into parts
+    auto load_state = [&](const float* src, int r0) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < X::kRows * kQuads; i += X::kThreads) {
+        const int r = i / kQuads, c = (i % kQuads) * 4;
+        put_parts<PP, X::kState>(smem + X::kOffS + (r * X::kPitch + c) * 2,
+                                 *reinterpret_cast<const float4*>(src + (r0 + r) * N + c));
+      }
+    };
+    const uint32_t rows = at_rows(lane, X::kPitch) + uint32_t(strip * 16 * X::kPitch) * 2u;
+    const uint32_t cols = at_channels(lane, X::kPitch) + uint32_t(slice * X::kCols) * 2u;
+    float q1[NT][4], k1[NT][4], k2[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) zero(q1[n]), zero(k1[n]), zero(k2[n]);
+    // S^T dy, S^T de
+#pragma unroll 1
+    for (int r0 = 0; r0 < N; r0 += X::kRows) {
+      if (r0 > 0) __syncthreads();
+      load_state(b.checkpoints + state_at, r0);
+      cp_async_wait_all();
+      __syncthreads();
+      product<PI, PP, NT, X::kRows, false, true>(q1, sb + X::kOffDy + rows + r0 * 2, X::kTile,
+                                                 X::kPitch, sb + X::kOffS + cols, X::kState,
+                                                 X::kPitch);
+      product<PP, PP, NT, X::kRows, false, true>(k1, sb + X::kOffDe + rows + r0 * 2, X::kTile,
+                                                 X::kPitch, sb + X::kOffS + cols, X::kState,
+                                                 X::kPitch);
+    }
+    // dD^T u, and <dD, S>
+    float inner = 0.f;
+#pragma unroll 1
+    for (int r0 = 0; r0 < N; r0 += X::kRows) {
+      __syncthreads();
+      load_state(b.dstates + state_at, r0);
+#pragma unroll 4
+      for (int i = threadIdx.x; i < X::kRows * kQuads; i += X::kThreads) {
+        const float4 x = reinterpret_cast<const float4*>(b.dstates + state_at + r0 * N)[i];
+        const float4 y = reinterpret_cast<const float4*>(b.checkpoints + state_at + r0 * N)[i];
+        inner = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, inner))));
+      }
+      __syncthreads();
+      product<PP, PP, NT, X::kRows, false, true>(k2, sb + X::kOffU + rows + r0 * 2, X::kTile,
+                                                 X::kPitch, sb + X::kOffS + cols, X::kState,
+                                                 X::kPitch);
+    }
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, m);
+    if (lane == 0) F.inner[warp] = inner;
+    float reach[2];  // exp(c_L - c_j) u_j . dD k_j of this thread's tokens
+    {
+      const int t = strip * 16 + g4;
+      const float since[2] = {F.since[t], F.since[t + 8]};
+      const float to_end[2] = {F.to_end[t], F.to_end[t + 8]};
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          q1[n][x] *= a.scale * since[x >> 1];
+          k1[n][x] *= -since[x >> 1];
+          k2[n][x] *= to_end[x >> 1];
+        }
+      dot_rows(k2, X::kOffK, reach);
+    }
+    // P and Z: this warp's tokens i, its share of the columns j
+    constexpr int kShares = X::kSlices < L / 16 ? X::kSlices : L / 16;
+    constexpr int NW = L / kShares / 8;  // column tiles of a warp
+    const bool shares = slice < kShares;
+    float pw[NW][4], zw[NW][4];
+#pragma unroll
+    for (int n = 0; n < NW; ++n) zero(pw[n]), zero(zw[n]);
+    const int j0 = slice * (L / kShares);
+    if (shares) {
+      const uint32_t us =
+          sb + X::kOffU + at_tokens(lane, X::kPitch) + uint32_t(j0 * X::kPitch) * 2u;
+      product<PI, PP, NW, N, false, false>(pw, sb + X::kOffDy + rows, X::kTile, X::kPitch, us,
+                                           X::kTile, X::kPitch);
+      product<PP, PP, NW, N, false, false>(zw, sb + X::kOffDe + rows, X::kTile, X::kPitch, us,
+                                           X::kTile, X::kPitch);
+    }
+    __syncthreads();  // dD's rows have been read: P takes their place
+#pragma unroll
+    for (int n = 0; n < (shares ? NW : 0); ++n)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int i = strip * 16 + g4 + z * 8, j = j0 + n * 8 + 2 * t4;
+        const Decay ci = F.c[i];
+        const float d0 = i >= j ? decay_between(ci, F.c[j]) : 0.f;
+        const float d1 = i >= j + 1 ? decay_between(ci, F.c[j + 1]) : 0.f;
+        uint32_t p[3];
+        const int to = (i * X::kPPitch + j) * 2;
+        split2(a.scale * d0 * pw[n][2 * z], a.scale * d1 * pw[n][2 * z + 1], p[0], p[1], p[2]);
+#pragma unroll
+        for (int x = 0; x < PP; ++x)
+          *reinterpret_cast<uint32_t*>(smem + X::kOffS + x * X::kPTile + to) = p[x];
+        split2(i > j ? d0 * zw[n][2 * z] : 0.f, i > j + 1 ? d1 * zw[n][2 * z + 1] : 0.f, p[0], p[1],
+               p[2]);
+#pragma unroll
+        for (int x = 0; x < PP; ++x)
+          *reinterpret_cast<uint32_t*>(smem + X::kOffZ + x * X::kPTile + to) = p[x];
+      }
+    __syncthreads();
+    // dq: + P K. dk, second part: - Z K (Z's sign is turned at the end). First: + P^T Q - Z^T K
+    const uint32_t prow = at_rows(lane, X::kPPitch) + uint32_t(strip * 16 * X::kPPitch) * 2u;
+    const uint32_t pcol = at_tokens(lane, X::kPPitch) + uint32_t(strip * 16) * 2u;
+    product<PP, PI, NT, L, false, true>(q1, sb + X::kOffS + prow, X::kPTile, X::kPPitch,
+                                        sb + X::kOffK + cols, X::kTile, X::kPitch);
+    product<PP, PI, NT, L, true, true>(k2, sb + X::kOffS + pcol, X::kPTile, X::kPPitch,
+                                       sb + X::kOffQ + cols, X::kTile, X::kPitch);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) k1[n][x] = -k1[n][x], k2[n][x] = -k2[n][x];
+    product<PP, PI, NT, L, false, true>(k1, sb + X::kOffZ + prow, X::kPTile, X::kPPitch,
+                                        sb + X::kOffK + cols, X::kTile, X::kPitch);
+    product<PP, PI, NT, L, true, true>(k2, sb + X::kOffZ + pcol, X::kPTile, X::kPPitch,
+                                       sb + X::kOffK + cols, X::kTile, X::kPitch);
+    // (k1 and k2 are the two parts of -dk now)
+    float dot_q[2], dot_1[2], dot_2[2];
+    dot_rows(q1, X::kOffQ, dot_q);
+    dot_rows(k1, X::kOffK, dot_1);
+    dot_rows(k2, X::kOffK, dot_2);
+    if (t4 == 0) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        F.dots[0][slice][strip * 16 + g4 + z * 8] = dot_q[z] + (dot_2[z] - dot_1[z]);
+        F.dots[1][slice][strip * 16 + g4 + z * 8] = reach[z];
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        dq[n][x] += q1[n][x];
+        dk[n][x] -= k1[n][x] + k2[n][x];
+      }
+    __syncthreads();
+    if (warp == 0) {
+      // dg: the sums over later tokens of the chunk, on top of <dD, S_L>
+      float base = 0.f, carry = 0.f;
+      for (int w = 0; w < X::kWarps; ++w) base += F.inner[w];
+      base *= F.since[L - 1];
+      float more = 0.f;
+#pragma unroll
+      for (int s = 0; s < L; s += 32)
+#pragma unroll
+        for (int w = 0; w < X::kSlices; ++w) more += F.dots[1][w][s + lane];
+#pragma unroll
+      for (int m = 16; m >= 1; m >>= 1) more += __shfl_xor_sync(0xffffffffu, more, m);
+      base += more;
+#pragma unroll
+      for (int s = L - 32; s >= 0; s -= 32) {
+        const int t = s + lane;
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < X::kSlices; ++w) x += F.dots[0][w][t];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const float above = __shfl_down_sync(0xffffffffu, x, d);
+          if (lane + d < 32) x += above;
+        }
+        x += carry;
+        carry = __shfl_sync(0xffffffffu, x, 0);
+        if (t < len) b.dg[(t0 + t) * a.H + h] = base + x;
+      }
+    }
+  }
+
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    const int t = strip * 16 + g4 + z * 8;
+    if (t >= len) continue;
+    const int64_t at = (t0 + t) * qk_row + int64_t(hk) * N + slice * X::kCols + 2 * t4;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if constexpr (X::kBf16) {
+        *reinterpret_cast<__nv_bfloat162*>(static_cast<T*>(b.dq) + at + n * 8) =
+            __float22bfloat162_rn(make_float2(dq[n][2 * z], dq[n][2 * z + 1]));
+        *reinterpret_cast<__nv_bfloat162*>(static_cast<T*>(b.dk) + at + n * 8) =
+            __float22bfloat162_rn(make_float2(dk[n][2 * z], dk[n][2 * z + 1]));
+      } else {
+        *reinterpret_cast<float2*>(static_cast<T*>(b.dq) + at + n * 8) =
+            make_float2(dq[n][2 * z], dq[n][2 * z + 1]);
+        *reinterpret_cast<float2*>(static_cast<T*>(b.dk) + at + n * 8) =
+            make_float2(dk[n][2 * z], dk[n][2 * z + 1]);
+      }
+    }
+  }
+}
+
+template <typename K>
+bool allow_smem(K* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+         cudaSuccess;
+}
+
+template <typename T, int N, int NC, int NG, int CTAS>
+int launch(const GdrBwdArgs& b, cudaStream_t stream) {
+  using X = Shape<T, N, NC, NG>;
+  using Y = Chunk<T, N>;
+  auto* chain = gdr_chain_kernel<T, N, NC, NG, CTAS>;
+  auto* rest = gdr_chunk_kernel<T, N>;
+  if (!allow_smem(chain, X::kSmem) || !allow_smem(rest, Y::kSmem)) return WKV_ERR_CUDA;
+  const unsigned grid = unsigned(int64_t(b.p.n_seqs) * b.p.H * (N / X::kVRows));
+  chain<<<grid, X::kThreads, X::kSmem, stream>>>(b);
+  if (cudaPeekAtLastError() != cudaSuccess) return WKV_ERR_CUDA;
+  rest<<<unsigned(gdr_chunks(b.p) * b.p.Hk), Y::kThreads, Y::kSmem, stream>>>(b);
+  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_gdr_backward(const GdrBwdArgs& b, cudaStream_t stream) {
+  if (b.p.bf16)
+    return b.p.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 2>(b, stream)
+                       : launch<__nv_bfloat16, 128, 4, 2, 2>(b, stream);
+  return b.p.N == 64 ? launch<float, 64, 4, 2, 1>(b, stream)
+                     : launch<float, 128, 4, 2, 1>(b, stream);
+}
+
+}  // namespace wkv

@@ -165,15 +165,40 @@ struct GdrArgs {
 int launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream);
 // In groups of 16 tokens on the matrix units. e (tokens, H, N) and checkpoints (chunks, H, N, N)
 // are what the backward reads: every token's error before its write, and the state entering
-// every chunk of kGdrChunk tokens of every sequence; null = not wanted.
-constexpr int kGdrChunk = 64;
+// every chunk of gdr_chunk() tokens of every sequence; null = not wanted.
 int launch_gdr_chunked(const GdrArgs& a, float* e, float* checkpoints, cudaStream_t stream);
-// Number of a sequence's first chunk. A sequence has a chunk more than its tokens fill, so that
-// the numbers of packed sequences follow from their offsets alone.
+// Tokens of a chunk: 32 where the chunk's operands would not fit shared memory at 64.
+__host__ __device__ constexpr int gdr_chunk(bool bf16, int N) { return !bf16 && N == 128 ? 32 : 64; }
+// Number of a sequence's first chunk. A packed sequence has a chunk more than its tokens fill, so
+// that the numbers follow from the offsets alone (which must not decrease).
 __host__ __device__ inline int64_t gdr_chunk_base(const GdrArgs& a, int seq, int64_t first_token) {
-  return a.offsets == nullptr ? int64_t(seq) * ((a.T + kGdrChunk - 1) / kGdrChunk)
-                              : first_token / kGdrChunk + seq;
+  const int chunk = gdr_chunk(a.bf16, a.N);
+  return a.offsets == nullptr ? int64_t(seq) * ((a.T + chunk - 1) / chunk)
+                              : first_token / chunk + seq;
 }
+__host__ __device__ inline int64_t gdr_chunks(const GdrArgs& a) {
+  const int chunk = gdr_chunk(a.bf16, a.N);
+  return a.offsets == nullptr ? int64_t(a.n_seqs) * ((int64_t(a.T) + chunk - 1) / chunk)
+                              : a.T / chunk + int64_t(a.n_seqs) + 1;
+}
+// Gradients. e, checkpoints: the forward's. du (tokens, H, N) and dstates (chunks, H, N, N):
+// scratch for the gradients of the written values and of the state leaving every chunk.
+struct GdrBwdArgs {
+  GdrArgs p;  // q, k, g, beta and sizes
+  const void* dy;
+  const float* e;
+  const float* checkpoints;
+  const float* ds1;
+  float* du;
+  float* dstates;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* dg;
+  float* dbeta;
+  float* ds0;
+};
+int launch_gdr_backward(const GdrBwdArgs& a, cudaStream_t stream);
 
 // Norm, gate, residual and next norm around a block (wkv_norm_gate.cu); null pointers are what
 // the entry points let a caller leave out.

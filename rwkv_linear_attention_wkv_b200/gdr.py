@@ -90,15 +90,7 @@ def _sequences(p):
     return p.n_seqs if p.seq_offsets else p.B
 
 
-def wkv_gdr_forward(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None, y=None,
-                    state_out=None, want_state=True, stream=None):
-    """Gated delta rule per head: q, k (B, T, Hk, N); v (B, T, H, N), bf16 or fp32; g
-    (log-decay) and beta (write strength) fp32 (B, T, H); N = 64 or 128, Hk divides H.
-
-    seq_offsets (int32, n + 1) packs n sequences into one row (B = 1). state: (sequences, H,
-    N, N) fp32 or None (zero). Returns (y, S_T), or (y, None) with want_state=False. state_out
-    may be `state` itself.
-    """
+def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_state):
     p = _problem(q, v, (0, 0), scale, seq_offsets)
     _inputs(q, k, v, g, beta, v.shape[:2])
     dev = v.device
@@ -113,9 +105,87 @@ def wkv_gdr_forward(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None, y
     if want_state:
         s1 = torch.empty(states, dtype=_F32, device=dev) if state_out is None else state_out
         _need(s1, "state_out", _F32, states, dev)
+    return p, y, s1, dev
+
+
+def wkv_gdr_forward(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None, y=None,
+                    state_out=None, want_state=True, stream=None):
+    """Gated delta rule per head: q, k (B, T, Hk, N); v (B, T, H, N), bf16 or fp32; g
+    (log-decay) and beta (write strength) fp32 (B, T, H); N = 64 or 128, Hk divides H.
+
+    seq_offsets (int32, n + 1) packs n sequences into one row (B = 1). state: (sequences, H,
+    N, N) fp32 or None (zero). Returns (y, S_T), or (y, None) with want_state=False. state_out
+    may be `state` itself.
+    """
+    p, y, s1, dev = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_state)
     _run("wkv_gdr_forward", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
          g.data_ptr(), beta.data_ptr(), y.data_ptr(), _at(state), _at(s1))
     return y, s1
+
+
+def _buffer(t, name, nbytes, device):
+    if t is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.device != device or not t.is_contiguous() or \
+            t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of at least {nbytes} bytes on "
+                         f"{device}")
+    return t
+
+
+def wkv_gdr_forward_checkpointed(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None, y=None,
+                                 state_out=None, want_state=True, workspace=None, stream=None):
+    """wkv_gdr_forward that also keeps what wkv_gdr_backward reads. Returns (y, S_T, workspace);
+    hand the workspace (it is only read there) to the backward of the same inputs. seq_offsets
+    must not decrease. state_out must not be `state` if `state` is needed again."""
+    p, y, s1, dev = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_state)
+    nbytes = int(lib.wkv_gdr_checkpoint_bytes(ctypes.byref(p)))
+    workspace = _buffer(workspace, "workspace", nbytes, dev)
+    _run("wkv_gdr_forward_checkpointed", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(),
+         v.data_ptr(), g.data_ptr(), beta.data_ptr(), y.data_ptr(), _at(state), _at(s1),
+         _at(workspace), workspace.numel() * workspace.element_size())
+    return y, s1, workspace
+
+
+def wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=None, scale=1.0, seq_offsets=None,
+                     want_dstate=True, grads=None, scratch=None, stream=None):
+    """Gradients of sum(dy * y) + sum(grad_state * S_T) for wkv_gdr_forward_checkpointed's call
+    with the same inputs, whose workspace this takes. Returns a dict of dq, dk, dv (as q, k, v),
+    dg, dbeta (fp32) and dstate (fp32; None with want_dstate=False). v is read for its shape only.
+
+    grads: such a dict to write into. Rows of the gradients that no packed sequence covers are
+    left as they were (uninitialised without `grads`)."""
+    p = _problem(q, v, (0, 0), scale, seq_offsets)
+    _inputs(q, k, v, g, beta, v.shape[:2])
+    dev = v.device
+    _need(dy, "dy", v.dtype, v.shape, dev)
+    states = torch.Size((_sequences(p), p.H, p.N, p.N))
+    if grad_state is not None:
+        _need(grad_state, "grad_state", _F32, states, dev)
+    shapes = {"dq": (q.dtype, q.shape), "dk": (q.dtype, q.shape), "dv": (v.dtype, v.shape),
+              "dg": (_F32, g.shape), "dbeta": (_F32, g.shape)}
+    if want_dstate:
+        shapes["dstate"] = (_F32, states)
+    if grads is None:
+        grads = {n: torch.empty(s, dtype=t, device=dev) for n, (t, s) in shapes.items()}
+    else:
+        for n, (t, s) in shapes.items():
+            _need(grads.get(n), n, t, s, dev)
+    nbytes = int(lib.wkv_gdr_checkpoint_bytes(ctypes.byref(p)))
+    if workspace is None:
+        raise TypeError("workspace must be the forward's")
+    _buffer(workspace, "workspace", nbytes, dev)
+    scratch = _buffer(scratch, "scratch",
+                      int(lib.wkv_gdr_backward_workspace_bytes(ctypes.byref(p))), dev)
+    _run("wkv_gdr_backward", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), g.data_ptr(),
+         beta.data_ptr(), dy.data_ptr(), _at(workspace), workspace.numel() * workspace.element_size(),
+         _at(grad_state), *[grads[n].data_ptr() for n in ("dq", "dk", "dv", "dg", "dbeta")],
+         _at(grads["dstate"]) if want_dstate else None, _at(scratch),
+         scratch.numel() * scratch.element_size())
+    return {n: grads.get(n) if n in shapes else None
+            for n in ("dq", "dk", "dv", "dg", "dbeta", "dstate")}
 
 
 def wkv_gdr_decode_step(q, k, v, g, beta, state, slots=None, scale=1.0, y=None, stream=None):

@@ -125,3 +125,53 @@ def test_binding_refusals(W):
         W.wkv_gdr_decode_step(q, q, q, g, g, q)
     with pytest.raises(ValueError, match="CUDA tensor"):
         W.wkv_gdr_decode_step(q[0], q[0], q[0], g[0], g[0], torch.zeros(2, 3, 64, 64))
+
+
+def test_training_pair_refusals(W):
+    ok, big = 4096, 1 << 40
+    f, b = W.lib.wkv_gdr_forward_checkpointed, W.lib.wkv_gdr_backward
+    size = W.lib.wkv_gdr_checkpoint_bytes(problem(W))
+    # e of 10 tokens, and one chunk per sequence
+    assert size == 4 * (2 * 5 * 4 * 64 + 2 * 4 * 64 * 64)
+    assert W.lib.wkv_gdr_backward_workspace_bytes(problem(W)) == size
+    # packed: 80 / 64 chunks, one more a sequence, and one; fp32 heads of 128 have chunks of 32
+    assert W.lib.wkv_gdr_checkpoint_bytes(problem(W, B=1, T=80, seq_offsets=ok, n_seqs=3)) == \
+        4 * (80 * 4 * 64 + 5 * 4 * 64 * 64)
+    assert W.lib.wkv_gdr_checkpoint_bytes(problem(W, T=80, N=128, dtype=0)) == \
+        4 * (2 * 80 * 4 * 128 + 2 * 3 * 4 * 128 * 128)
+    for over in (dict(B=0), dict(T=0), dict(H=0), dict(N=32), dict(B=-1)):
+        assert W.lib.wkv_gdr_checkpoint_bytes(problem(W, **over)) == 0
+    fa = [ok] * 6 + [None, None, ok, size, None]
+    put = lambda args, i, x: args[:i] + [x] + args[i + 1:]  # noqa: E731
+    for i in range(6):
+        assert f(problem(W), *put(fa, i, None)) == 1, i
+    assert f(problem(W), *put(fa, 8, None)) == 1
+    assert f(problem(W), *put(fa, 9, size - 1)) == 1
+    for i in (0, 1, 2, 5, 6, 7, 8):
+        assert f(problem(W), *put(fa, i, ok + 8)) == 2, i
+    assert f(problem(W, N=96), *fa) == 5 and f(problem(W, dtype=3), *fa) == 1
+    assert f(problem(W, B=0), *fa) == 0
+    ba = [ok] * 6 + [size, None] + [ok] * 5 + [None, ok, size, None]
+    assert b(None, *ba) == 1
+    for i in (0, 1, 2, 3, 4, 5, 8, 9, 10, 11, 12, 14):
+        assert b(problem(W), *put(ba, i, None)) == 1, i
+    for i in (6, 15):
+        assert b(problem(W), *put(ba, i, size - 1)) == 1, i
+    for i in (0, 1, 4, 5, 7, 8, 9, 10, 13, 14):
+        assert b(problem(W), *put(ba, i, ok + 8)) == 2, i
+    for i in (2, 3, 11, 12):
+        assert b(problem(W), *put(ba, i, ok + 2)) == 2, i
+    assert b(problem(W, N=96), *ba) == 5 and b(problem(W, H=5), *ba) == 5
+    assert b(problem(W, H=0), *ba) == 0
+    # more chunks x query/key heads than a grid holds
+    assert b(problem(W, B=1 << 20, T=1 << 15, H=8, Hk=8), *put(put(ba, 6, big << 20), 15, big << 20)) == 5
+
+
+def test_training_pair_binding_refusals(W):
+    x = ref.inputs((1, 4), 2, 4, 64, torch.float32, 5)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        W.wkv_gdr_forward_checkpointed(*x)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        W.wkv_gdr_backward(*x, x[2], torch.zeros(10))
+    with pytest.raises(TypeError, match="must be a torch.Tensor"):
+        W.wkv_gdr_backward(None, *x[1:], x[2], None)
