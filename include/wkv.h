@@ -360,9 +360,9 @@ WKV_API int wkv_gdr_forward(const wkv_gdr_problem* p, const void* q, const void*
 /*
  * The pair for training. The forward also keeps, in `checkpoints` (device, 16-byte aligned,
  * wkv_gdr_checkpoint_bytes(p) bytes: 0 where there is nothing to keep), every token's e_t in
- * fp32 and the state entering every 64 tokens of a sequence (32 for fp32 heads of 128).
- * The backward gives the gradients of sum(dy y) + sum(ds1 s1) from the same q, k, g, beta (v is
- * not needed again) and those checkpoints, which it only reads: dq, dk as q; dv as v; dg, dbeta
+ * fp32, the state entering every 64 tokens of a sequence (32 for fp32 heads of 128) and the one
+ * leaving it. The backward gives the gradients of sum(dy y) + sum(ds1 s1) from the same inputs
+ * and those checkpoints, which it only reads: dq, dk as q; dv as v; dg, dbeta
  * fp32 (B, T, H); ds0 as the states. ds1 NULL = zero; ds0 NULL = not wanted, and may be ds1. dq
  * and dk are summed over the value heads that share them; every sum has a fixed order. No
  * gradient may overlap an input or another. workspace: device, 16-byte aligned, scratch of
@@ -377,7 +377,7 @@ WKV_API int wkv_gdr_forward_checkpointed(const wkv_gdr_problem* p, const void* q
                                          const float* s0, float* s1, void* checkpoints,
                                          size_t checkpoint_bytes, cudaStream_t stream);
 WKV_API int wkv_gdr_backward(const wkv_gdr_problem* p, const void* q, const void* k,
-                             const float* g, const float* beta, const void* dy,
+                             const void* v, const float* g, const float* beta, const void* dy,
                              const void* checkpoints, size_t checkpoint_bytes, const float* ds1,
                              void* dq, void* dk, void* dv, float* dg, float* dbeta, float* ds0,
                              void* workspace, size_t workspace_bytes, cudaStream_t stream);

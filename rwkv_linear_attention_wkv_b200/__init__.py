@@ -61,7 +61,7 @@ _SIGS = {
     "wkv_gdr_checkpoint_bytes": ([_P], ctypes.c_size_t),
     "wkv_gdr_backward_workspace_bytes": ([_P], ctypes.c_size_t),
     "wkv_gdr_forward_checkpointed": ([_P] * 10 + [ctypes.c_size_t, _P], ctypes.c_int),
-    "wkv_gdr_backward": ([_P] * 7 + [ctypes.c_size_t] + [_P] * 8 + [ctypes.c_size_t, _P],
+    "wkv_gdr_backward": ([_P] * 8 + [ctypes.c_size_t] + [_P] * 8 + [ctypes.c_size_t, _P],
                          ctypes.c_int),
     "wkv_gdr_decode_step": ([_P] * 8 + [_I, _P, _P], ctypes.c_int),
     "wkv_norm_gate_forward": ([_P] * 9 + [_P], ctypes.c_int),

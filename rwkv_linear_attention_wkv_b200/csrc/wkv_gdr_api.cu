@@ -111,14 +111,14 @@ WKV_API int wkv_gdr_forward_checkpointed(const wkv_gdr_problem* p, const void* q
 }
 
 WKV_API int wkv_gdr_backward(const wkv_gdr_problem* p, const void* q, const void* k,
-                             const float* g, const float* beta, const void* dy,
+                             const void* v, const float* g, const float* beta, const void* dy,
                              const void* checkpoints, size_t checkpoint_bytes, const float* ds1,
                              void* dq, void* dk, void* dv, float* dg, float* dbeta, float* ds0,
                              void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   bool empty;
   if (int rc = check_problem(p, &empty)) return rc;
   if (empty) return WKV_OK;
-  for (const void* x : {q, k, dy, checkpoints, (const void*)dq, (const void*)dk, (const void*)dv,
+  for (const void* x : {q, k, v, dy, checkpoints, (const void*)dq, (const void*)dk, (const void*)dv,
                         (const void*)ds1, (const void*)ds0, (const void*)workspace})
     if (!aligned(x, 16)) return WKV_ERR_ALIGNMENT;
   for (const void* x : {(const void*)g, (const void*)beta, (const void*)dg, (const void*)dbeta})
@@ -127,7 +127,7 @@ WKV_API int wkv_gdr_backward(const wkv_gdr_problem* p, const void* q, const void
   b.p = args_of(p);
   if (p->T == 0)
     return pass_state(ds1, ds0, size_t(b.p.n_seqs) * b.p.H * b.p.N * b.p.N * 4, stream);
-  for (const void* x : {q, k, (const void*)g, (const void*)beta, dy, checkpoints, (const void*)dq,
+  for (const void* x : {q, k, v, (const void*)g, (const void*)beta, dy, checkpoints, (const void*)dq,
                         (const void*)dk, (const void*)dv, (const void*)dg, (const void*)dbeta,
                         (const void*)workspace})
     if (x == nullptr) return WKV_ERR_INVALID_ARG;
@@ -135,7 +135,7 @@ WKV_API int wkv_gdr_backward(const wkv_gdr_problem* p, const void* q, const void
     return WKV_ERR_INVALID_ARG;
   if (gdr_chunks(b.p) > ((int64_t(1) << 31) - 1) / b.p.Hk) return WKV_ERR_UNSUPPORTED;
   const Saved s = saved_of(b.p);
-  b.p.q = q; b.p.k = k; b.p.g = g; b.p.beta = beta;
+  b.p.q = q; b.p.k = k; b.p.v = v; b.p.g = g; b.p.beta = beta;
   b.dy = dy;
   b.e = static_cast<const float*>(checkpoints);
   b.checkpoints = b.e + s.tokens;

@@ -15,13 +15,14 @@
 //      dq = scale C S^T dy + P K
 //      dk = [exp(c_L - c) dD^T u + P^T Q - Z^T K] + [-C S^T de - Z K]
 //      dbeta_j = du_j . e_j
-//      dg_t = <dD, S_L> + sum_{i >= t} q_i . dq_i + k_i . [second] - k_i . [first],
-//    since c_i enters with a plus where token i reads and a minus where it writes.
+//      dg_t = <dD, S_L> + sum_{i >= t} q_i . dq_i - v_i . dv_i,   S_L the state that leaves.
+//    (c_i enters with a plus where token i reads: q_i . dq_i, and de_i . (e_i - v_i) in the error;
+//    and with a minus where it writes: u_i . du_i = e_i . de_i.)
 //
 // Rounding: the chain keeps the full three-part products everywhere (its results feed fp32
-// gradients of states). In the second kernel bf16 problems take two parts (2^-17 a factor), well
-// below the bf16 rounding of dq and dk; fp32 problems take three.
-#include <algorithm>
+// gradients of states), and so does the second kernel for fp32 problems and in whatever leads to
+// dg. What only the bf16 dq and dk see takes two parts (2^-17 a factor).
+#include <type_traits>
 
 #include "wkv_gdr.cuh"
 
@@ -288,7 +289,8 @@ struct Chunk {
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int kLen = gdr_chunk(kBf16, N);    // tokens
   static constexpr int kIn = kBf16 ? 1 : 3;           // parts of q, k, dy
-  static constexpr int kParts = kBf16 ? 2 : 3;        // parts of u, de, states, P, Z
+  static constexpr int kParts = kBf16 ? 2 : 3;        // parts that dk needs of u, de, states, P, Z
+  static constexpr int kAll = 3;                      // parts that dg needs of u, S, P
   static constexpr int kCols = N == 64 ? 64 : kBf16 ? 64 : 32;  // columns of a warp
   static constexpr int kSlices = N / kCols;           // warps that share a strip of 16 tokens
   static constexpr int kWarps = kLen / 16 * kSlices;
@@ -303,21 +305,30 @@ struct Chunk {
   static constexpr int kOffQ = kOffK + kIn * kTile;
   static constexpr int kOffDy = kOffQ + kIn * kTile;
   static constexpr int kOffU = kOffDy + kIn * kTile;
-  static constexpr int kOffDe = kOffU + kParts * kTile;
-  // a state's rows; later P in the same place
-  static constexpr int kOffS = kOffDe + kParts * kTile;
-  static constexpr int kOffZ = kOffS + kParts * (kState > kPTile ? kState : kPTile);
-  static constexpr int kOffF = kOffZ + kParts * kPTile;  // floats, see Floats
+  static constexpr int kOffDe = kOffU + kAll * kTile;   // later Z
+  static constexpr int kOffS = kOffDe + kParts * kTile;  // 64 rows of a state; later P
+  static constexpr int kOffF = kOffS + kAll * kState;    // floats
+  static_assert(kPTile <= kTile && kPTile <= kState, "Z and P fit where de and the states were");
   struct Floats {
     Decay c[kLen];
     float beta[kLen];
     float to_end[kLen];      // exp(c_L - c_j)
     float since[kLen];       // C_i
-    float dots[3][kSlices][kLen];
-    float inner[kWarps];     // <dD, S> by warp
+    float written[kLen];     // v . dv
+    float read[kSlices][kLen];  // q . dq by slice of the columns
+    float inner[kWarps];     // <dD, S_L> by warp
   };
   static constexpr int kSmem = kOffF + int(sizeof(Floats));
 };
+
+__device__ __forceinline__ float4 load4(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  const float2 lo = unpack(r.x), hi = unpack(r.y);
+  return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
 
 // One value as PARTS bf16 parts, four at a time, PART bytes apart.
 template <int PARTS, int PART>
@@ -346,8 +357,10 @@ __device__ __forceinline__ void mma_parts(float (&c)[NT][4], int n, const uint32
 }
 
 // c (16 rows x 8 NT columns) += A B over LEN: A's fragments at `a` + 32 bytes a step, B's rows at
-// `b` + 16 rows a step, columns 32 bytes apart a tile pair. TA: A stored transposed.
-template <int PA, int PB, int NT, int LEN, bool TA, bool TB>
+// `b` + 16 rows a step, columns 32 bytes apart a tile pair. TA: A stored transposed. EXACT: every
+// step of 16 is summed on its own and added in fp32 (the matrix instruction truncates as it adds
+// to a large sum: over the 24 to 48 adds of a product that costs two bits).
+template <int PA, int PB, int NT, int LEN, bool TA, bool TB, bool EXACT>
 __device__ __forceinline__ void product(float (&c)[NT][4], uint32_t a, int a_part, int a_pitch,
                                         uint32_t b, int b_part, int b_pitch) {
 #pragma unroll 2
@@ -370,7 +383,16 @@ __device__ __forceinline__ void product(float (&c)[NT][4], uint32_t a, int a_par
         else     // rows are the product's columns
           ldsm4(bp[p], b + p * b_part + n * 8 * b_pitch * 2 + l * 2);
       }
-      mma_parts<PA, PB, NT>(c, n, ap, bp);
+      if (EXACT) {
+        float d[2][4];
+        zero(d[0]);
+        zero(d[1]);
+        mma_parts<PA, PB, 2>(d, 0, ap, bp);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) c[n][x] += d[0][x], c[n + 1][x] += d[1][x];
+      } else {
+        mma_parts<PA, PB, NT>(c, n, ap, bp);
+      }
     }
   }
 }
@@ -385,7 +407,8 @@ template <typename T, int N>
 __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
     gdr_chunk_kernel(GdrBwdArgs b) {
   using X = Chunk<T, N>;
-  constexpr int PI = X::kIn, PP = X::kParts, NT = X::kCols / 8, L = X::kLen;
+  constexpr int PI = X::kIn, PP = X::kParts, PA = X::kAll, NT = X::kCols / 8, L = X::kLen;
+  constexpr bool kExact = !X::kBf16;  // of what only dk sees
   extern __shared__ __align__(128) unsigned char smem[];
   typename X::Floats& F = *reinterpret_cast<typename X::Floats*>(smem + X::kOffF);
   const GdrArgs& a = b.p;
@@ -400,10 +423,11 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
   int seq = -1, chunk = 0, len = 0;
   int64_t t0 = 0;
   if (a.offsets == nullptr) {
-    const int per = (a.T + L - 1) / L;
+    const int per = (a.T + L - 1) / L + 1;
     seq = int(slot / per);
     chunk = int(slot % per);
     t0 = sequence(a, seq, len);
+    if (chunk == per - 1) return;
   } else {
     for (int s0 = 0; s0 < a.n_seqs && seq < 0; s0 += 32) {
       bool mine = false;
@@ -498,33 +522,41 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
       F.beta[t] = t < len ? a.beta[(t0 + t) * a.H + h] : 0.f;
     }
     __syncthreads();
-    // u, de, dbeta: a token's row lies in kQuads adjacent lanes
+    // u, de, dbeta, v . dv: a token's row lies in kQuads adjacent lanes
 #pragma unroll 4
     for (int i = threadIdx.x; i < L * kQuads; i += X::kThreads) {
       const int t = i / kQuads, c = (i % kQuads) * 4;
-      float4 e = make_float4(0.f, 0.f, 0.f, 0.f), d = e;
+      float4 e = make_float4(0.f, 0.f, 0.f, 0.f), d = e, v = e;
       const int64_t at = (t0 + t) * v_row + int64_t(h) * N + c;
       if (t < len) {
         e = *reinterpret_cast<const float4*>(b.e + at);
         d = *reinterpret_cast<const float4*>(b.du + at);
+        v = load4(static_cast<const T*>(a.v) + at);
       }
       const float be = F.beta[t];
       float s = fmaf(e.x, d.x, fmaf(e.y, d.y, fmaf(e.z, d.z, e.w * d.w)));
+      float w = fmaf(v.x, d.x, fmaf(v.y, d.y, fmaf(v.z, d.z, v.w * d.w)));
 #pragma unroll
-      for (int m = kQuads / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-      if (c == 0 && t < len) b.dbeta[(t0 + t) * a.H + h] = s;
+      for (int m = kQuads / 2; m >= 1; m >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, m);
+        w += __shfl_xor_sync(0xffffffffu, w, m);
+      }
+      if (c == 0) {
+        F.written[t] = be * w;
+        if (t < len) b.dbeta[(t0 + t) * a.H + h] = s;
+      }
       const int to = (t * X::kPitch + c) * 2;
-      put_parts<PP, X::kTile>(smem + X::kOffU + to,
+      put_parts<PA, X::kTile>(smem + X::kOffU + to,
                               make_float4(be * e.x, be * e.y, be * e.z, be * e.w));
       put_parts<PP, X::kTile>(smem + X::kOffDe + to,
                               make_float4(be * d.x, be * d.y, be * d.z, be * d.w));
     }
     // 64 rows of a state into parts
-    auto load_state = [&](const float* src, int r0) {
+    auto load_state = [&](const float* src, int r0, auto parts) {
 #pragma unroll 4
       for (int i = threadIdx.x; i < X::kRows * kQuads; i += X::kThreads) {
         const int r = i / kQuads, c = (i % kQuads) * 4;
-        put_parts<PP, X::kState>(smem + X::kOffS + (r * X::kPitch + c) * 2,
+        put_parts<decltype(parts)::value, X::kState>(smem + X::kOffS + (r * X::kPitch + c) * 2,
                                  *reinterpret_cast<const float4*>(src + (r0 + r) * N + c));
       }
     };
@@ -537,38 +569,39 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
 #pragma unroll 1
     for (int r0 = 0; r0 < N; r0 += X::kRows) {
       if (r0 > 0) __syncthreads();
-      load_state(b.checkpoints + state_at, r0);
+      load_state(b.checkpoints + state_at, r0, std::integral_constant<int, PA>());
       cp_async_wait_all();
       __syncthreads();
-      product<PI, PP, NT, X::kRows, false, true>(q1, sb + X::kOffDy + rows + r0 * 2, X::kTile,
-                                                 X::kPitch, sb + X::kOffS + cols, X::kState,
-                                                 X::kPitch);
-      product<PP, PP, NT, X::kRows, false, true>(k1, sb + X::kOffDe + rows + r0 * 2, X::kTile,
-                                                 X::kPitch, sb + X::kOffS + cols, X::kState,
-                                                 X::kPitch);
+      product<PI, PA, NT, X::kRows, false, true, true>(q1, sb + X::kOffDy + rows + r0 * 2, X::kTile,
+                                                       X::kPitch, sb + X::kOffS + cols, X::kState,
+                                                       X::kPitch);
+      product<PP, PP, NT, X::kRows, false, true, kExact>(
+          k1, sb + X::kOffDe + rows + r0 * 2, X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
+          X::kPitch);
     }
-    // dD^T u, and <dD, S>
+    // dD^T u, and <dD, S_L>
     float inner = 0.f;
+    const int64_t next_at = state_at + int64_t(a.H) * N * N;
 #pragma unroll 1
     for (int r0 = 0; r0 < N; r0 += X::kRows) {
       __syncthreads();
-      load_state(b.dstates + state_at, r0);
+      load_state(b.dstates + state_at, r0, std::integral_constant<int, PP>());
 #pragma unroll 4
       for (int i = threadIdx.x; i < X::kRows * kQuads; i += X::kThreads) {
         const float4 x = reinterpret_cast<const float4*>(b.dstates + state_at + r0 * N)[i];
-        const float4 y = reinterpret_cast<const float4*>(b.checkpoints + state_at + r0 * N)[i];
+        const float4 y = reinterpret_cast<const float4*>(b.checkpoints + next_at + r0 * N)[i];
         inner = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, inner))));
       }
       __syncthreads();
-      product<PP, PP, NT, X::kRows, false, true>(k2, sb + X::kOffU + rows + r0 * 2, X::kTile,
-                                                 X::kPitch, sb + X::kOffS + cols, X::kState,
-                                                 X::kPitch);
+      product<PP, PP, NT, X::kRows, false, true, kExact>(
+          k2, sb + X::kOffU + rows + r0 * 2, X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
+          X::kPitch);
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, m);
     if (lane == 0) F.inner[warp] = inner;
-    float reach[2];  // exp(c_L - c_j) u_j . dD k_j of this thread's tokens
     {
+      // dk = k2 - k1 from here on
       const int t = strip * 16 + g4;
       const float since[2] = {F.since[t], F.since[t + 8]};
       const float to_end[2] = {F.to_end[t], F.to_end[t + 8]};
@@ -577,10 +610,9 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           q1[n][x] *= a.scale * since[x >> 1];
-          k1[n][x] *= -since[x >> 1];
+          k1[n][x] *= since[x >> 1];
           k2[n][x] *= to_end[x >> 1];
         }
-      dot_rows(k2, X::kOffK, reach);
     }
     // P and Z: this warp's tokens i, its share of the columns j
     constexpr int kShares = X::kSlices < L / 16 ? X::kSlices : L / 16;
@@ -593,12 +625,12 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
     if (shares) {
       const uint32_t us =
           sb + X::kOffU + at_tokens(lane, X::kPitch) + uint32_t(j0 * X::kPitch) * 2u;
-      product<PI, PP, NW, N, false, false>(pw, sb + X::kOffDy + rows, X::kTile, X::kPitch, us,
-                                           X::kTile, X::kPitch);
-      product<PP, PP, NW, N, false, false>(zw, sb + X::kOffDe + rows, X::kTile, X::kPitch, us,
-                                           X::kTile, X::kPitch);
+      product<PI, PA, NW, N, false, false, true>(pw, sb + X::kOffDy + rows, X::kTile, X::kPitch, us,
+                                                 X::kTile, X::kPitch);
+      product<PP, PP, NW, N, false, false, kExact>(zw, sb + X::kOffDe + rows, X::kTile, X::kPitch,
+                                                   us, X::kTile, X::kPitch);
     }
-    __syncthreads();  // dD's rows have been read: P takes their place
+    __syncthreads();  // dD's rows and de have been read: P and Z take their places
 #pragma unroll
     for (int n = 0; n < (shares ? NW : 0); ++n)
 #pragma unroll
@@ -611,69 +643,50 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
         const int to = (i * X::kPPitch + j) * 2;
         split2(a.scale * d0 * pw[n][2 * z], a.scale * d1 * pw[n][2 * z + 1], p[0], p[1], p[2]);
 #pragma unroll
-        for (int x = 0; x < PP; ++x)
+        for (int x = 0; x < PA; ++x)
           *reinterpret_cast<uint32_t*>(smem + X::kOffS + x * X::kPTile + to) = p[x];
         split2(i > j ? d0 * zw[n][2 * z] : 0.f, i > j + 1 ? d1 * zw[n][2 * z + 1] : 0.f, p[0], p[1],
                p[2]);
 #pragma unroll
         for (int x = 0; x < PP; ++x)
-          *reinterpret_cast<uint32_t*>(smem + X::kOffZ + x * X::kPTile + to) = p[x];
+          *reinterpret_cast<uint32_t*>(smem + X::kOffDe + x * X::kPTile + to) = p[x];
       }
     __syncthreads();
-    // dq: + P K. dk, second part: - Z K (Z's sign is turned at the end). First: + P^T Q - Z^T K
+    // dq: + P K; k2: + P^T Q; k1: + Z K + Z^T K
     const uint32_t prow = at_rows(lane, X::kPPitch) + uint32_t(strip * 16 * X::kPPitch) * 2u;
     const uint32_t pcol = at_tokens(lane, X::kPPitch) + uint32_t(strip * 16) * 2u;
-    product<PP, PI, NT, L, false, true>(q1, sb + X::kOffS + prow, X::kPTile, X::kPPitch,
-                                        sb + X::kOffK + cols, X::kTile, X::kPitch);
-    product<PP, PI, NT, L, true, true>(k2, sb + X::kOffS + pcol, X::kPTile, X::kPPitch,
-                                       sb + X::kOffQ + cols, X::kTile, X::kPitch);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) k1[n][x] = -k1[n][x], k2[n][x] = -k2[n][x];
-    product<PP, PI, NT, L, false, true>(k1, sb + X::kOffZ + prow, X::kPTile, X::kPPitch,
-                                        sb + X::kOffK + cols, X::kTile, X::kPitch);
-    product<PP, PI, NT, L, true, true>(k2, sb + X::kOffZ + pcol, X::kPTile, X::kPPitch,
-                                       sb + X::kOffK + cols, X::kTile, X::kPitch);
-    // (k1 and k2 are the two parts of -dk now)
-    float dot_q[2], dot_1[2], dot_2[2];
-    dot_rows(q1, X::kOffQ, dot_q);
-    dot_rows(k1, X::kOffK, dot_1);
-    dot_rows(k2, X::kOffK, dot_2);
+    product<PA, PI, NT, L, false, true, true>(q1, sb + X::kOffS + prow, X::kPTile, X::kPPitch,
+                                              sb + X::kOffK + cols, X::kTile, X::kPitch);
+    product<PP, PI, NT, L, true, true, kExact>(k2, sb + X::kOffS + pcol, X::kPTile, X::kPPitch,
+                                               sb + X::kOffQ + cols, X::kTile, X::kPitch);
+    product<PP, PI, NT, L, false, true, kExact>(k1, sb + X::kOffDe + prow, X::kPTile, X::kPPitch,
+                                                sb + X::kOffK + cols, X::kTile, X::kPitch);
+    product<PP, PI, NT, L, true, true, kExact>(k1, sb + X::kOffDe + pcol, X::kPTile, X::kPPitch,
+                                               sb + X::kOffK + cols, X::kTile, X::kPitch);
+    float read[2];
+    dot_rows(q1, X::kOffQ, read);
     if (t4 == 0) {
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        F.dots[0][slice][strip * 16 + g4 + z * 8] = dot_q[z] + (dot_2[z] - dot_1[z]);
-        F.dots[1][slice][strip * 16 + g4 + z * 8] = reach[z];
-      }
+      for (int z = 0; z < 2; ++z) F.read[slice][strip * 16 + g4 + z * 8] = read[z];
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         dq[n][x] += q1[n][x];
-        dk[n][x] -= k1[n][x] + k2[n][x];
+        dk[n][x] += k2[n][x] - k1[n][x];
       }
     __syncthreads();
     if (warp == 0) {
       // dg: the sums over later tokens of the chunk, on top of <dD, S_L>
       float base = 0.f, carry = 0.f;
       for (int w = 0; w < X::kWarps; ++w) base += F.inner[w];
-      base *= F.since[L - 1];
-      float more = 0.f;
-#pragma unroll
-      for (int s = 0; s < L; s += 32)
-#pragma unroll
-        for (int w = 0; w < X::kSlices; ++w) more += F.dots[1][w][s + lane];
-#pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) more += __shfl_xor_sync(0xffffffffu, more, m);
-      base += more;
 #pragma unroll
       for (int s = L - 32; s >= 0; s -= 32) {
         const int t = s + lane;
-        float x = 0.f;
+        float x = -F.written[t];
 #pragma unroll
-        for (int w = 0; w < X::kSlices; ++w) x += F.dots[0][w][t];
+        for (int w = 0; w < X::kSlices; ++w) x += F.read[w][t];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const float above = __shfl_down_sync(0xffffffffu, x, d);

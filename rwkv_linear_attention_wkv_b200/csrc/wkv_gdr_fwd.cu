@@ -255,6 +255,12 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG>::kThreads, CTAS)
     }
     __syncthreads();
   }
+  if (checkpoints != nullptr && len > 0) {
+    constexpr int kChunk = gdr_chunk(X::kBf16, N);
+    put_state<N>(checkpoints + ((gdr_chunk_base(a, seq, t0) + (len + kChunk - 1) / kChunk) * a.H +
+                                h) * N * N + r0 * N,
+                 S, lane);
+  }
   if (a.s1 != nullptr) put_state<N>(a.s1 + state_at, S, lane);
 }
 

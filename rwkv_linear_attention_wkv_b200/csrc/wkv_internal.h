@@ -165,26 +165,27 @@ struct GdrArgs {
 int launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream);
 // In groups of 16 tokens on the matrix units. e (tokens, H, N) and checkpoints (chunks, H, N, N)
 // are what the backward reads: every token's error before its write, and the state entering
-// every chunk of gdr_chunk() tokens of every sequence; null = not wanted.
+// every chunk of gdr_chunk() tokens of every sequence, and leaving the last; null = not wanted.
 int launch_gdr_chunked(const GdrArgs& a, float* e, float* checkpoints, cudaStream_t stream);
 // Tokens of a chunk: 32 where the chunk's operands would not fit shared memory at 64.
 __host__ __device__ constexpr int gdr_chunk(bool bf16, int N) { return !bf16 && N == 128 ? 32 : 64; }
-// Number of a sequence's first chunk. A packed sequence has a chunk more than its tokens fill, so
-// that the numbers follow from the offsets alone (which must not decrease).
+// Number of a sequence's first chunk. After a sequence's chunks comes one that holds the state
+// leaving the last; a packed sequence has two chunks more than whole ones, so that the numbers
+// follow from the offsets alone (which must not decrease).
 __host__ __device__ inline int64_t gdr_chunk_base(const GdrArgs& a, int seq, int64_t first_token) {
   const int chunk = gdr_chunk(a.bf16, a.N);
-  return a.offsets == nullptr ? int64_t(seq) * ((a.T + chunk - 1) / chunk)
-                              : first_token / chunk + seq;
+  return a.offsets == nullptr ? int64_t(seq) * ((int64_t(a.T) + chunk - 1) / chunk + 1)
+                              : first_token / chunk + 2 * int64_t(seq);
 }
 __host__ __device__ inline int64_t gdr_chunks(const GdrArgs& a) {
   const int chunk = gdr_chunk(a.bf16, a.N);
-  return a.offsets == nullptr ? int64_t(a.n_seqs) * ((int64_t(a.T) + chunk - 1) / chunk)
-                              : a.T / chunk + int64_t(a.n_seqs) + 1;
+  return a.offsets == nullptr ? int64_t(a.n_seqs) * ((int64_t(a.T) + chunk - 1) / chunk + 1)
+                              : a.T / chunk + 2 * int64_t(a.n_seqs) + 1;
 }
 // Gradients. e, checkpoints: the forward's. du (tokens, H, N) and dstates (chunks, H, N, N):
 // scratch for the gradients of the written values and of the state leaving every chunk.
 struct GdrBwdArgs {
-  GdrArgs p;  // q, k, g, beta and sizes
+  GdrArgs p;  // q, k, v, g, beta and sizes
   const void* dy;
   const float* e;
   const float* checkpoints;

@@ -153,7 +153,7 @@ def wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=None, scale=1.0
                      want_dstate=True, grads=None, scratch=None, stream=None):
     """Gradients of sum(dy * y) + sum(grad_state * S_T) for wkv_gdr_forward_checkpointed's call
     with the same inputs, whose workspace this takes. Returns a dict of dq, dk, dv (as q, k, v),
-    dg, dbeta (fp32) and dstate (fp32; None with want_dstate=False). v is read for its shape only.
+    dg, dbeta (fp32) and dstate (fp32; None with want_dstate=False).
 
     grads: such a dict to write into. Rows of the gradients that no packed sequence covers are
     left as they were (uninitialised without `grads`)."""
@@ -179,8 +179,8 @@ def wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=None, scale=1.0
     _buffer(workspace, "workspace", nbytes, dev)
     scratch = _buffer(scratch, "scratch",
                       int(lib.wkv_gdr_backward_workspace_bytes(ctypes.byref(p))), dev)
-    _run("wkv_gdr_backward", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), g.data_ptr(),
-         beta.data_ptr(), dy.data_ptr(), _at(workspace), workspace.numel() * workspace.element_size(),
+    _run("wkv_gdr_backward", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         g.data_ptr(), beta.data_ptr(), dy.data_ptr(), _at(workspace), workspace.numel() * workspace.element_size(),
          _at(grad_state), *[grads[n].data_ptr() for n in ("dq", "dk", "dv", "dg", "dbeta")],
          _at(grads["dstate"]) if want_dstate else None, _at(scratch),
          scratch.numel() * scratch.element_size())

@@ -131,14 +131,14 @@ def test_training_pair_refusals(W):
     ok, big = 4096, 1 << 40
     f, b = W.lib.wkv_gdr_forward_checkpointed, W.lib.wkv_gdr_backward
     size = W.lib.wkv_gdr_checkpoint_bytes(problem(W))
-    # e of 10 tokens, and one chunk per sequence
-    assert size == 4 * (2 * 5 * 4 * 64 + 2 * 4 * 64 * 64)
+    # e of 10 tokens, and the states entering and leaving each sequence
+    assert size == 4 * (2 * 5 * 4 * 64 + 4 * 4 * 64 * 64)
     assert W.lib.wkv_gdr_backward_workspace_bytes(problem(W)) == size
-    # packed: 80 / 64 chunks, one more a sequence, and one; fp32 heads of 128 have chunks of 32
+    # packed: 80 / 64 chunks, two more a sequence, and one; fp32 heads of 128 have chunks of 32
     assert W.lib.wkv_gdr_checkpoint_bytes(problem(W, B=1, T=80, seq_offsets=ok, n_seqs=3)) == \
-        4 * (80 * 4 * 64 + 5 * 4 * 64 * 64)
+        4 * (80 * 4 * 64 + 8 * 4 * 64 * 64)
     assert W.lib.wkv_gdr_checkpoint_bytes(problem(W, T=80, N=128, dtype=0)) == \
-        4 * (2 * 80 * 4 * 128 + 2 * 3 * 4 * 128 * 128)
+        4 * (2 * 80 * 4 * 128 + 2 * 4 * 4 * 128 * 128)
     for over in (dict(B=0), dict(T=0), dict(H=0), dict(N=32), dict(B=-1)):
         assert W.lib.wkv_gdr_checkpoint_bytes(problem(W, **over)) == 0
     fa = [ok] * 6 + [None, None, ok, size, None]
@@ -151,20 +151,20 @@ def test_training_pair_refusals(W):
         assert f(problem(W), *put(fa, i, ok + 8)) == 2, i
     assert f(problem(W, N=96), *fa) == 5 and f(problem(W, dtype=3), *fa) == 1
     assert f(problem(W, B=0), *fa) == 0
-    ba = [ok] * 6 + [size, None] + [ok] * 5 + [None, ok, size, None]
+    ba = [ok] * 7 + [size, None] + [ok] * 5 + [None, ok, size, None]
     assert b(None, *ba) == 1
-    for i in (0, 1, 2, 3, 4, 5, 8, 9, 10, 11, 12, 14):
+    for i in (0, 1, 2, 3, 4, 5, 6, 9, 10, 11, 12, 13, 15):
         assert b(problem(W), *put(ba, i, None)) == 1, i
-    for i in (6, 15):
+    for i in (7, 16):
         assert b(problem(W), *put(ba, i, size - 1)) == 1, i
-    for i in (0, 1, 4, 5, 7, 8, 9, 10, 13, 14):
+    for i in (0, 1, 2, 5, 6, 8, 9, 10, 11, 14, 15):
         assert b(problem(W), *put(ba, i, ok + 8)) == 2, i
-    for i in (2, 3, 11, 12):
+    for i in (3, 4, 12, 13):
         assert b(problem(W), *put(ba, i, ok + 2)) == 2, i
     assert b(problem(W, N=96), *ba) == 5 and b(problem(W, H=5), *ba) == 5
     assert b(problem(W, H=0), *ba) == 0
     # more chunks x query/key heads than a grid holds
-    assert b(problem(W, B=1 << 20, T=1 << 15, H=8, Hk=8), *put(put(ba, 6, big << 20), 15, big << 20)) == 5
+    assert b(problem(W, B=1 << 20, T=1 << 15, H=8, Hk=8), *put(put(ba, 7, big << 20), 16, big << 20)) == 5
 
 
 def test_training_pair_binding_refusals(W):
