@@ -1,4 +1,4 @@
-"""The WKV operator as a PyTorch autograd function (argument marshalling only).
+"""The library's operators as PyTorch autograd functions (argument marshalling only).
 
 The news page "RWKV CUDA linear attention GPU" describes the CUDA operator being used
 from PyTorch through an autograd function whose forward and backward are fused kernels.
@@ -13,10 +13,15 @@ library's kernels, on the current CUDA stream, in fp32.
 
 w is the positive decay itself (the per-token factor is e^{-w}), so w's gradient is with
 respect to w, not log w. r may be None (no gate).
+
+`gated_delta_rule` and `norm_gate` are the matrix-state update with a decay and a write strength
+per token, and the norms, gate and residual around a block, in the same manner (bf16 or fp32).
 """
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import wkv_backward_checkpointed, wkv_forward_checkpointed
+from . import (wkv_backward_checkpointed, wkv_forward_checkpointed, wkv_gdr_backward,
+               wkv_gdr_forward_checkpointed, wkv_norm_gate_backward, wkv_norm_gate_forward)
 
 
 class WKVFunction(torch.autograd.Function):
@@ -42,3 +47,80 @@ class WKVFunction(torch.autograd.Function):
 def wkv(w, u, k, v, r=None):
     """Differentiable WKV: see WKVFunction."""
     return WKVFunction.apply(w, u, k, v, r)
+
+
+class GatedDeltaRuleFunction(torch.autograd.Function):
+    """(y, final states) of the gated delta rule with the library's gradients for q, k, v, g, beta
+    and the initial states."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, state, scale, seq_offsets):
+        q, k, v, g, beta = (t.contiguous() for t in (q, k, v, g, beta))
+        state = None if state is None else state.contiguous()
+        # tokens that no packed sequence covers are not written
+        y = torch.empty_like(v) if seq_offsets is None else torch.zeros_like(v)
+        y, last, workspace = wkv_gdr_forward_checkpointed(q, k, v, g, beta, state=state, scale=scale,
+                                                          seq_offsets=seq_offsets, y=y)
+        ctx.save_for_backward(q, k, v, g, beta, seq_offsets, workspace)
+        ctx.scale, ctx.has_state = scale, state is not None
+        ctx.set_materialize_grads(False)
+        return y, last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dlast):
+        if dy is None and dlast is None:
+            return (None,) * 8
+        q, k, v, g, beta, seq_offsets, workspace = ctx.saved_tensors
+        dy = torch.zeros_like(v) if dy is None else dy.contiguous()
+        dlast = None if dlast is None else dlast.contiguous()
+        grads = None
+        if seq_offsets is not None:
+            grads = {"d" + n: torch.zeros_like(t) for n, t in
+                     (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta))}
+            if ctx.has_state:
+                H, N = v.shape[2:]
+                grads["dstate"] = torch.empty(seq_offsets.numel() - 1, H, N, N, device=v.device)
+        d = wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=dlast, scale=ctx.scale,
+                             seq_offsets=seq_offsets, want_dstate=ctx.has_state, grads=grads)
+        return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], d["dstate"], None, None
+
+
+def gated_delta_rule(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None):
+    """Differentiable wkv_gdr_forward: (y, final states), with gradients for q, k, v, g, beta and
+    state, through both results. With seq_offsets, y and the gradients are zero at tokens that no
+    sequence covers. Types and shapes as wkv_gdr_forward; inputs may be non-contiguous."""
+    return GatedDeltaRuleFunction.apply(q, k, v, g, beta, state, scale, seq_offsets)
+
+
+class NormGateFunction(torch.autograd.Function):
+    """(out, y) of wkv_norm_gate_forward with the library's gradients."""
+
+    @staticmethod
+    def forward(ctx, h, weight, gate, x, scale, next_weight, group, act, eps):
+        h, weight, gate, x, scale, next_weight = (
+            None if t is None else t.contiguous() for t in (h, weight, gate, x, scale, next_weight))
+        out, y = wkv_norm_gate_forward(h, weight, gate=gate, x=x, scale=scale,
+                                       next_weight=next_weight, group=group, act=act, eps=eps)
+        ctx.save_for_backward(h, weight, gate, x, scale, next_weight)
+        ctx.how = dict(group=group, act=act, eps=eps)
+        ctx.set_materialize_grads(False)
+        return out, y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, dy):
+        if dout is None and dy is None:
+            return (None,) * 9
+        h, weight, gate, x, scale, next_weight = ctx.saved_tensors
+        g = wkv_norm_gate_backward(h, weight, None if dout is None else dout.contiguous(), gate=gate,
+                                   x=x, scale=scale, next_weight=next_weight,
+                                   dy=None if dy is None else dy.contiguous(), **ctx.how)
+        return (g["dh"], g["dweight"], g["dgate"], g["dx"], g["dscale"], g["dnext_weight"], None,
+                None, None)
+
+
+def norm_gate(h, weight=None, gate=None, x=None, scale=None, next_weight=None, group=None,
+              act="silu", eps=1e-6):
+    """Differentiable wkv_norm_gate_forward: (out, y), y None without next_weight."""
+    return NormGateFunction.apply(h, weight, gate, x, scale, next_weight, group, act, eps)
