@@ -28,6 +28,11 @@ constexpr int kTeamsMax = 8;      // rows a CTA works on at once
 
 enum GroupMode { kRow, kLanes, kAny };
 
+// CTAs on an SM at once. Forward, bf16: two of 512 threads, so that one loads while the other sums
+// (64 registers hold the next row and this one; fp32 rows need twice as many, and one CTA has as
+// many bytes in flight). Backward: one; its sums over rows and five inputs take 128 to 168.
+constexpr int fwd_ctas(bool bf16, int threads) { return bf16 && threads <= 512 ? 2 : 1; }
+
 struct Eight {
   float v[kE];
 };
@@ -92,18 +97,35 @@ __device__ __forceinline__ void store(T* p, const Eight& x, const Place<VEC>& pl
   }
 }
 
+// A weight's row in shared memory, in the order in which a team's threads take it: [8][threads],
+// or, for adjacent channels, [2][threads][4].
 template <bool VEC>
-__device__ __forceinline__ Eight params(const float* p, const Place<VEC>& pl, float none) {
+__device__ __forceinline__ Eight params(const float* row, const Place<VEC>& pl) {
   Eight x;
+  if (VEC) {
+    const float4 a = *reinterpret_cast<const float4*>(row + pl.c0 / 2);
+    const float4 b = *reinterpret_cast<const float4*>(row + 4 * pl.step + pl.c0 / 2);
+    x.v[0] = a.x; x.v[1] = a.y; x.v[2] = a.z; x.v[3] = a.w;
+    x.v[4] = b.x; x.v[5] = b.y; x.v[6] = b.z; x.v[7] = b.w;
+  } else {
 #pragma unroll
-  for (int i = 0; i < kE; ++i) x.v[i] = !pl.in(i) ? 0.f : p ? p[pl.at(i)] : none;
+    for (int i = 0; i < kE; ++i) x.v[i] = row[pl.c0 + i * pl.step];
+  }
   return x;
+}
+template <bool VEC>
+__device__ __forceinline__ void put_params(float* row, const float* p, int step, int C) {
+  for (int c = threadIdx.x; c < kE * step; c += blockDim.x) {
+    const int to = VEC ? (c % kE / 4) * 4 * step + c / kE * 4 + c % 4 : c;
+    row[to] = c >= C ? 0.f : p ? p[c] : 1.f;
+  }
 }
 
 // The warps that hold one row: their sums go through shared memory (two slots in turn, so that
 // one barrier a sum is enough).
 struct Team {
   int warps, warp, lane, id;
+  float* weights;    // [3][8 x threads of a team]: weight, scale, next weight
   float2* slots;     // [2][32]
   float* parts;      // kAny: one value per channel (VEC: per eight) and one per group
   int turn = 0;
@@ -115,22 +137,36 @@ struct Team {
       asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(warps * 32) : "memory");
   }
 
-  __device__ float2 sum(float a, float b) {
+  __device__ static void lanes(float& a) {
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, m);
-      b += __shfl_xor_sync(0xffffffffu, b, m);
-    }
+    for (int m = 16; m >= 1; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
+  }
+
+  __device__ float sum(float a) {
+    lanes(a);
+    if (warps == 1) return a;
+    float2* s = slots + 32 * turn;
+    turn ^= 1;
+    if (lane == 0) s[warp].x = a;
+    sync();
+    a = lane < warps ? s[lane].x : 0.f;
+    lanes(a);
+    return a;
+  }
+
+  __device__ float2 sum(float a, float b) {
+    lanes(a);
+    lanes(b);
     if (warps == 1) return make_float2(a, b);
     float2* s = slots + 32 * turn;
     turn ^= 1;
     if (lane == 0) s[warp] = make_float2(a, b);
     sync();
-    a = b = 0.f;
-    for (int w = 0; w < warps; ++w) {
-      a += s[w].x;
-      b += s[w].y;
-    }
+    const float2 mine = lane < warps ? s[lane] : make_float2(0.f, 0.f);
+    a = mine.x;
+    b = mine.y;
+    lanes(a);
+    lanes(b);
     return make_float2(a, b);
   }
 };
@@ -145,7 +181,7 @@ __device__ __forceinline__ Eight group_sum(const Eight& x, Team& t, const Place<
 #pragma unroll
     for (int i = 0; i < kE; ++i) s += x.v[i];
     if (MODE == kRow) {
-      s = t.sum(s, 0.f).x;
+      s = t.sum(s);
     } else {
       for (int m = group / kE / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     }
@@ -172,11 +208,11 @@ __device__ __forceinline__ Eight group_sum(const Eight& x, Team& t, const Place<
   return out;
 }
 
-// act(z) and its slope; act: 0 none, 1 sigmoid, 2 silu.
-__device__ __forceinline__ void gate_of(float z, int act, float& a, float& slope) {
-  const float s = 1.f / (1.f + expf(-z)), d = s * (1.f - s);
-  a = act == WKV_ACT_SILU ? z * s : s;
-  slope = act == WKV_ACT_SILU ? fmaf(z, d, s) : d;
+// sigmoid(z) by the exponential and reciprocal instructions: e^-z is off by |z| 2^-24 of itself,
+// the sigmoid by at most s (1 - s) |z| 2^-24 < 2^-26. (expf and a division: 15 instructions more,
+// a third of a forward row.)
+__device__ __forceinline__ float sigmoid_of(float z) {
+  return __fdividef(1.f, 1.f + ex2(z * -1.4426950408889634f));
 }
 
 template <bool VEC>
@@ -188,8 +224,10 @@ __device__ __forceinline__ void make_team(int team_warps, int C, Team& t, Place<
   t.warp = warp % team_warps;
   t.lane = threadIdx.x & 31;
   const int teams = (blockDim.x >> 5) / team_warps;
-  t.slots = reinterpret_cast<float2*>(smem_ng) + 64 * t.id;
-  t.parts = smem_ng + 128 * teams + 2 * C * t.id;
+  const int wide = team_warps * 32 * kE;
+  t.weights = smem_ng;
+  t.slots = reinterpret_cast<float2*>(smem_ng + 3 * wide) + 64 * t.id;
+  t.parts = smem_ng + 3 * wide + 128 * teams + 2 * C * t.id;
   const int at = t.warp * 32 + t.lane;
   pl.C = C;
   pl.step = team_warps * 32;
@@ -197,13 +235,17 @@ __device__ __forceinline__ void make_team(int team_warps, int C, Team& t, Place<
 }
 
 template <typename T, bool VEC, GroupMode MODE, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_fwd_kernel(NormGateArgs a, int team_warps) {
+__global__ void __launch_bounds__(MAX_THREADS, fwd_ctas(sizeof(T) == 2, MAX_THREADS))
+    norm_gate_fwd_kernel(NormGateArgs a, int team_warps) {
   Team t;
   Place<VEC> pl;
   make_team<VEC>(team_warps, a.C, t, pl);
   const int teams = (blockDim.x >> 5) / team_warps;
-  const Eight w = params(a.weight, pl, 1.f), s = params(a.scale, pl, 1.f),
-              wn = params(a.next_weight, pl, 1.f);
+  const int wide = pl.step * kE;
+  put_params<VEC>(t.weights, a.weight, pl.step, a.C);
+  put_params<VEC>(t.weights + wide, a.scale, pl.step, a.C);
+  put_params<VEC>(t.weights + 2 * wide, a.next_weight, pl.step, a.C);
+  __syncthreads();
   const T *h = static_cast<const T*>(a.h), *z = static_cast<const T*>(a.gate),
           *x = static_cast<const T*>(a.x);
   const float inv_group = 1.f / a.group, inv_c = 1.f / a.C;
@@ -218,16 +260,15 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_fwd_kernel(NormGateA
   if (row < a.R) fetch(row);
   for (; row < a.R; row += stride) {
     const Eight hv = widen<T>(hr);
-    Eight m;
+    Eight m = params<VEC>(t.weights, pl);
 #pragma unroll
-    for (int i = 0; i < kE; ++i) m.v[i] = hv.v[i] * w.v[i];
+    for (int i = 0; i < kE; ++i) m.v[i] *= hv.v[i];
     if (z) {
       const Eight zv = widen<T>(zr);
 #pragma unroll
       for (int i = 0; i < kE; ++i) {
-        float act, slope;
-        gate_of(zv.v[i], a.act, act, slope);
-        m.v[i] *= act;
+        const float sig = sigmoid_of(zv.v[i]);
+        m.v[i] *= a.act == WKV_ACT_SILU ? zv.v[i] * sig : sig;
       }
     }
     Eight xv{};
@@ -238,16 +279,19 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_fwd_kernel(NormGateA
     for (int i = 0; i < kE; ++i) sq.v[i] = hv.v[i] * hv.v[i];
     const Eight ms = group_sum<VEC, MODE>(sq, t, pl, a.group);
 #pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      m.v[i] *= rsqrtf(fmaf(ms.v[i], inv_group, a.eps));
-      if (x) m.v[i] = fmaf(s.v[i], m.v[i], xv.v[i]);
+    for (int i = 0; i < kE; ++i) m.v[i] *= rsqrtf(fmaf(ms.v[i], inv_group, a.eps));
+    if (x) {
+      const Eight s = params<VEC>(t.weights + wide, pl);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) m.v[i] = fmaf(s.v[i], m.v[i], xv.v[i]);
     }
     store<T, VEC>(static_cast<T*>(a.out) + row * a.C, m, pl);
     if (a.y) {
       float q = 0.f;
 #pragma unroll
       for (int i = 0; i < kE; ++i) q = fmaf(m.v[i], m.v[i], q);
-      const float r2 = rsqrtf(fmaf(t.sum(q, 0.f).x, inv_c, a.eps));
+      const float r2 = rsqrtf(fmaf(t.sum(q), inv_c, a.eps));
+      const Eight wn = params<VEC>(t.weights + 2 * wide, pl);
 #pragma unroll
       for (int i = 0; i < kE; ++i) m.v[i] *= r2 * wn.v[i];
       store<T, VEC>(static_cast<T*>(a.y) + row * a.C, m, pl);
@@ -261,8 +305,11 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_bwd_kernel(NormGateA
   Place<VEC> pl;
   make_team<VEC>(team_warps, a.C, t, pl);
   const int teams = (blockDim.x >> 5) / team_warps;
-  const Eight w = params(a.weight, pl, 1.f), s = params(a.scale, pl, 1.f),
-              wn = params(a.next_weight, pl, 1.f);
+  const int wide = pl.step * kE;
+  put_params<VEC>(t.weights, a.weight, pl.step, a.C);
+  put_params<VEC>(t.weights + wide, a.scale, pl.step, a.C);
+  put_params<VEC>(t.weights + 2 * wide, a.next_weight, pl.step, a.C);
+  __syncthreads();
   const T *h = static_cast<const T*>(a.h), *z = static_cast<const T*>(a.gate),
           *x = static_cast<const T*>(a.x), *dout = static_cast<const T*>(a.dout),
           *dy = static_cast<const T*>(a.dy);
@@ -280,14 +327,20 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_bwd_kernel(NormGateA
   };
   if (first < a.R) fetch(first);
   for (int64_t row = first; row < a.R; row += stride) {
-    Eight hn = widen<T>(hr), act, slope, d{}, out{};
-#pragma unroll
-    for (int i = 0; i < kE; ++i) act.v[i] = 1.f;
+    Eight hn = widen<T>(hr), sig{}, d{}, out{};
+    const Raw<T> zk = zr;
     if (z) {
-      const Eight zv = widen<T>(zr);
+      const Eight zv = widen<T>(zk);
 #pragma unroll
-      for (int i = 0; i < kE; ++i) gate_of(zv.v[i], a.act, act.v[i], slope.v[i]);
+      for (int i = 0; i < kE; ++i) sig.v[i] = sigmoid_of(zv.v[i]);
     }
+    const bool silu = a.act == WKV_ACT_SILU;
+    auto act_of = [&] {
+      Eight act = silu ? widen<T>(zk) : sig;
+#pragma unroll
+      for (int i = 0; i < kE; ++i) act.v[i] = !z ? 1.f : silu ? act.v[i] * sig.v[i] : act.v[i];
+      return act;
+    };
     if (x) out = widen<T>(xr);
     if (dout) d = widen<T>(dor);
     Eight dn{};
@@ -297,16 +350,22 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_bwd_kernel(NormGateA
 #pragma unroll
     for (int i = 0; i < kE; ++i) r1.v[i] = hn.v[i] * hn.v[i];
     r1 = group_sum<VEC, MODE>(r1, t, pl, a.group);
+    const Eight w = params<VEC>(t.weights, pl);
     float so = 0.f, sd = 0.f;
+    {
+      const Eight s = params<VEC>(t.weights + wide, pl), wn = params<VEC>(t.weights + 2 * wide, pl);
+      const Eight act = act_of();
 #pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      r1.v[i] = rsqrtf(fmaf(r1.v[i], inv_group, a.eps));
-      hn.v[i] *= r1.v[i];
-      out.v[i] = fmaf(s.v[i], act.v[i] * w.v[i] * hn.v[i], out.v[i]);
-      so = fmaf(out.v[i], out.v[i], so);
-      sd = fmaf(out.v[i], dn.v[i] * wn.v[i], sd);
+      for (int i = 0; i < kE; ++i) {
+        r1.v[i] = rsqrtf(fmaf(r1.v[i], inv_group, a.eps));
+        hn.v[i] *= r1.v[i];
+        out.v[i] = fmaf(s.v[i], act.v[i] * w.v[i] * hn.v[i], out.v[i]);
+        so = fmaf(out.v[i], out.v[i], so);
+        sd = fmaf(out.v[i], dn.v[i] * wn.v[i], sd);
+      }
     }
     if (dy) {
+      const Eight wn = params<VEC>(t.weights + 2 * wide, pl);
       const float2 both = t.sum(so, sd);
       const float r2 = rsqrtf(fmaf(both.x, inv_c, a.eps));
       const float pull = r2 * r2 * both.y * inv_c;  // <dy w', out r2> r2 / C
@@ -317,34 +376,49 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_bwd_kernel(NormGateA
       }
     }
     if (a.dx) store<T, VEC>(static_cast<T*>(a.dx) + row * a.C, d, pl);
-    Eight n, p;
+    Eight n, p, dz;
+    const Eight s = params<VEC>(t.weights + wide, pl), act = act_of();
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
       const float dm = d.v[i] * s.v[i], ah = act.v[i] * hn.v[i];
       ds.v[i] = fmaf(d.v[i], ah * w.v[i], ds.v[i]);
       dw.v[i] = fmaf(dm, ah, dw.v[i]);
-      slope.v[i] = z ? dm * w.v[i] * hn.v[i] * slope.v[i] : 0.f;
-      n.v[i] = dm * act.v[i] * w.v[i];
+      n.v[i] = dm * w.v[i];
+      // silu' = sig + z sig (1 - sig), sigmoid' = sig (1 - sig)
+      const float off = 1.f - sig.v[i];
+      dz.v[i] = n.v[i] * hn.v[i] * (silu ? fmaf(act.v[i], off, sig.v[i]) : sig.v[i] * off);
+      n.v[i] *= act.v[i];
       p.v[i] = n.v[i] * hn.v[i];
     }
-    if (a.dgate) store<T, VEC>(static_cast<T*>(a.dgate) + row * a.C, slope, pl);
+    if (a.dgate) store<T, VEC>(static_cast<T*>(a.dgate) + row * a.C, dz, pl);
     p = group_sum<VEC, MODE>(p, t, pl, a.group);
 #pragma unroll
     for (int i = 0; i < kE; ++i)
       n.v[i] = r1.v[i] * fmaf(-hn.v[i], p.v[i] * inv_group, n.v[i]);
     store<T, VEC>(static_cast<T*>(a.dh) + row * a.C, n, pl);
   }
-  float* line = a.partial + first * 3 * a.C;  // [dw, ds, dw'] of this team
+  // the teams' sums added up in order where the weights were, a line a CTA
+  float* const sums = t.weights;
+  for (int id = 0; id < teams; ++id) {
+    __syncthreads();
+    if (t.id != id) continue;
 #pragma unroll
-  for (int i = 0; i < kE; ++i)
-    if (pl.in(i)) {
-      line[pl.at(i)] = dw.v[i];
-      line[a.C + pl.at(i)] = ds.v[i];
-      line[2 * a.C + pl.at(i)] = dwn.v[i];
+    for (int i = 0; i < kE; ++i) {
+      const int c = pl.at(i);
+      if (!pl.in(i)) continue;
+      sums[c] = id == 0 ? dw.v[i] : sums[c] + dw.v[i];
+      sums[wide + c] = id == 0 ? ds.v[i] : sums[wide + c] + ds.v[i];
+      sums[2 * wide + c] = id == 0 ? dwn.v[i] : sums[2 * wide + c] + dwn.v[i];
     }
+  }
+  __syncthreads();
+  float* line = a.partial + int64_t(blockIdx.x) * 3 * a.C;  // [dw, ds, dw'] of this CTA
+  for (int c = threadIdx.x; c < a.C; c += blockDim.x)
+#pragma unroll
+    for (int j = 0; j < 3; ++j) line[j * a.C + c] = sums[j * wide + c];
 }
 
-// The teams' lines added up: 32 columns x 8 slices of the lines a CTA, the slices in order.
+// The CTAs' lines added up: 32 columns x 8 slices of the lines a CTA, the slices in order.
 __global__ void __launch_bounds__(256) norm_gate_sum_kernel(const float* partial, int lines, int C,
                                                             float* dw, float* ds, float* dwn) {
   __shared__ float part[8][32];
@@ -380,34 +454,36 @@ int sm_count() {
   return n;
 }
 
-// Threads of a CTA: rows of 256 channels or less four to a CTA, wider ones as many as make 384
-// threads; CTAs: enough for `threads` threads on every SM, each of whose teams has a row.
-Plan plan_of(int64_t R, int C, int group, bool vec, int threads, int sms) {
+// Rows of a CTA: as many as make 512 threads (forward) or 384 (backward), CTAs: as many as the
+// GPU holds at once, as long as each team has a row.
+Plan plan_of(int64_t R, int C, int group, bool vec, bool bf16, bool backward, int sms) {
   Plan p;
   p.team_warps = (C + 32 * kE - 1) / (32 * kE);
-  p.teams = std::max(1, std::min(kTeamsMax, 12 / p.team_warps));
-  const int per_sm = std::max(1, threads / (32 * p.team_warps * p.teams));
+  p.teams = std::max(1, std::min(kTeamsMax, (backward ? 12 : 16) / p.team_warps));
+  const int threads = 32 * p.team_warps * p.teams;
+  const int per_sm = backward ? 1 : fwd_ctas(bf16, threads);
   p.grid = int(std::min<int64_t>((R + p.teams - 1) / p.teams, int64_t(sms) * per_sm));
   const int lanes = group / kE;
   const bool pow2 = (lanes & (lanes - 1)) == 0;
   p.mode = group == C ? kRow
            : vec && group % kE == 0 && lanes <= 32 && pow2 ? kLanes
                                                            : kAny;
-  p.smem = size_t(p.teams) * (512 + (p.mode == kAny ? 8 * size_t(C) : 0));
+  p.smem = size_t(p.teams) * (512 + (p.mode == kAny ? 8 * size_t(C) : 0)) +
+           size_t(p.team_warps) * 32 * kE * 12;
   return p;
 }
 
-constexpr int kFwdThreads = 1536, kBwdThreads = 768;
-
-// Rows of up to 4096 channels fit 512 threads, which leaves a thread the 128 registers that the
-// weights, the sums over rows and the next row need; wider ones take 1024 and spill some.
+// Backward: rows of up to 12 warps fit 384 threads, which leaves a thread 168 registers for
+// the sums over rows, this row and the next; up to 16 warps take 512 threads and 128; wider
+// ones take 1024 threads and spill.
 template <typename T, bool VEC, GroupMode MODE>
 int run(const NormGateArgs& a, const Plan& p, bool backward, cudaStream_t stream) {
-  auto* kernel = p.team_warps * p.teams <= 16
-                     ? (backward ? norm_gate_bwd_kernel<T, VEC, MODE, 512>
-                                 : norm_gate_fwd_kernel<T, VEC, MODE, 512>)
-                     : (backward ? norm_gate_bwd_kernel<T, VEC, MODE, 1024>
-                                 : norm_gate_fwd_kernel<T, VEC, MODE, 1024>);
+  const int warps = p.team_warps * p.teams;
+  auto* kernel = backward ? (warps <= 12   ? norm_gate_bwd_kernel<T, VEC, MODE, 384>
+                             : warps <= 16 ? norm_gate_bwd_kernel<T, VEC, MODE, 512>
+                                           : norm_gate_bwd_kernel<T, VEC, MODE, 1024>)
+                          : (warps <= 16 ? norm_gate_fwd_kernel<T, VEC, MODE, 512>
+                                         : norm_gate_fwd_kernel<T, VEC, MODE, 1024>);
   if (p.smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem)) !=
           cudaSuccess)
@@ -443,15 +519,15 @@ int64_t norm_gate_max_c() { return kMaxC; }
 // size does not depend on the device that is current).
 size_t norm_gate_workspace_bytes(int64_t R, int64_t C) {
   if (R <= 0 || C <= 0 || C > kMaxC) return 0;
-  const Plan p = plan_of(R, int(C), int(C), true, kBwdThreads, 160);
-  return size_t(p.grid) * p.teams * 3 * size_t(C) * sizeof(float);
+  const Plan p = plan_of(R, int(C), int(C), true, true, true, 160);
+  return size_t(p.grid) * 3 * size_t(C) * sizeof(float);
 }
 
 int launch_norm_gate_forward(const NormGateArgs& a, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return WKV_ERR_CUDA;
   const bool vec = vectors(a);
-  const Plan p = plan_of(a.R, a.C, a.group, vec, kFwdThreads, sms);
+  const Plan p = plan_of(a.R, a.C, a.group, vec, a.bf16, false, sms);
   return a.bf16 ? pick<__nv_bfloat16>(a, p, vec, false, stream)
                 : pick<float>(a, p, vec, false, stream);
 }
@@ -460,13 +536,13 @@ int launch_norm_gate_backward(const NormGateArgs& a, cudaStream_t stream) {
   const int sms = std::min(sm_count(), 160);
   if (sms <= 0) return WKV_ERR_CUDA;
   const bool vec = vectors(a);
-  const Plan p = plan_of(a.R, a.C, a.group, vec, kBwdThreads, sms);
+  const Plan p = plan_of(a.R, a.C, a.group, vec, a.bf16, true, sms);
   const int rc = a.bf16 ? pick<__nv_bfloat16>(a, p, vec, true, stream)
                         : pick<float>(a, p, vec, true, stream);
   if (rc != WKV_OK) return rc;
   if (!a.dweight && !a.dscale && !a.dnext_weight) return WKV_OK;
   norm_gate_sum_kernel<<<dim3((a.C + 31) / 32, 3), 256, 0, stream>>>(
-      a.partial, p.grid * p.teams, a.C, a.dweight, a.dscale, a.dnext_weight);
+      a.partial, p.grid, a.C, a.dweight, a.dscale, a.dnext_weight);
   return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
 }
 
