@@ -291,7 +291,10 @@ struct Chunk {
   static constexpr int kIn = kBf16 ? 1 : 3;           // parts of q, k, dy
   static constexpr int kParts = kBf16 ? 2 : 3;        // parts that dk needs of u, de, states, P, Z
   static constexpr int kAll = 3;                      // parts that dg needs of u, S, P
-  static constexpr int kCols = N == 64 ? 64 : kBf16 ? 64 : 32;  // columns of a warp
+  // Columns of a warp: such that an SM holds 16 warps (two CTAs of 8 for bf16 heads of 64, else one
+  // of 16) at 128 registers.
+  static constexpr int kCols = kBf16 ? 32 : 16;
+  static constexpr int kCtas = kBf16 && N == 64 ? 2 : 1;
   static constexpr int kSlices = N / kCols;           // warps that share a strip of 16 tokens
   static constexpr int kWarps = kLen / 16 * kSlices;
   static constexpr int kThreads = 32 * kWarps;
@@ -360,11 +363,13 @@ __device__ __forceinline__ void mma_parts(float (&c)[NT][4], int n, const uint32
 // `b` + 16 rows a step, columns 32 bytes apart a tile pair. TA: A stored transposed. EXACT: every
 // step of 16 is summed on its own and added in fp32 (the matrix instruction truncates as it adds
 // to a large sum: over the 24 to 48 adds of a product that costs two bits).
-template <int PA, int PB, int NT, int LEN, bool TA, bool TB, bool EXACT>
-__device__ __forceinline__ void product(float (&c)[NT][4], uint32_t a, int a_part, int a_pitch,
-                                        uint32_t b, int b_part, int b_pitch) {
+// Only the steps of [l0, l1) and the first `cols` column tiles are taken.
+template <int PA, int PB, int NT, bool TA, bool TB, bool EXACT>
+__device__ __forceinline__ void product(float (&c)[NT][4], int l0, int l1, uint32_t a, int a_part,
+                                        int a_pitch, uint32_t b, int b_part, int b_pitch,
+                                        int cols = NT) {
 #pragma unroll 2
-  for (int l = 0; l < LEN; l += 16) {
+  for (int l = l0; l < l1; l += 16) {
     uint32_t ap[PA][4];
 #pragma unroll
     for (int p = 0; p < PA; ++p) {
@@ -375,6 +380,7 @@ __device__ __forceinline__ void product(float (&c)[NT][4], uint32_t a, int a_par
     }
 #pragma unroll
     for (int n = 0; n < NT; n += 2) {
+      if (n >= cols) continue;
       uint32_t bp[PB][4];
 #pragma unroll
       for (int p = 0; p < PB; ++p) {
@@ -404,7 +410,7 @@ __device__ __forceinline__ uint32_t at_rows(int lane, int pitch) {
 }
 
 template <typename T, int N>
-__global__ void __launch_bounds__(Chunk<T, N>::kThreads)
+__global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     gdr_chunk_kernel(GdrBwdArgs b) {
   using X = Chunk<T, N>;
   constexpr int PI = X::kIn, PP = X::kParts, PA = X::kAll, NT = X::kCols / 8, L = X::kLen;
@@ -501,6 +507,35 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
 #pragma unroll 1
   for (int h = hk * G; h < hk * G + G; ++h) {
     const int64_t state_at = (slot * a.H + h) * N * N;
+    // what the head needs first, on its way before anything is waited for
+    constexpr int kTok = L * kQuads / X::kThreads, kSt = X::kRows * kQuads / X::kThreads;
+    float4 er[kTok], dr[kTok], vr[kTok], sr[kSt];
+#pragma unroll
+    for (int x = 0; x < kTok; ++x) {
+      const int i = threadIdx.x + x * X::kThreads, t = i / kQuads;
+      const int64_t at = (t0 + t) * v_row + int64_t(h) * N + (i % kQuads) * 4;
+      er[x] = dr[x] = vr[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < len) {
+        er[x] = *reinterpret_cast<const float4*>(b.e + at);
+        dr[x] = *reinterpret_cast<const float4*>(b.du + at);
+        vr[x] = load4(static_cast<const T*>(a.v) + at);
+      }
+    }
+    // 64 rows of a state, from global memory and into parts
+    auto fetch_state = [&](const float* src, int r0) {
+#pragma unroll
+      for (int x = 0; x < kSt; ++x)
+        sr[x] = reinterpret_cast<const float4*>(src + r0 * N)[threadIdx.x + x * X::kThreads];
+    };
+    auto store_state = [&](auto parts) {
+#pragma unroll
+      for (int x = 0; x < kSt; ++x) {
+        const int i = threadIdx.x + x * X::kThreads;
+        put_parts<decltype(parts)::value, X::kState>(
+            smem + X::kOffS + (i / kQuads * X::kPitch + (i % kQuads) * 4) * 2, sr[x]);
+      }
+    };
+    fetch_state(b.checkpoints + state_at, 0);
     __syncthreads();  // the last head's tiles have been read
     load_input(static_cast<const T*>(b.dy) + t0 * v_row + int64_t(h) * N, v_row, X::kOffDy);
     if (threadIdx.x < 32) {
@@ -523,16 +558,10 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
     }
     __syncthreads();
     // u, de, dbeta, v . dv: a token's row lies in kQuads adjacent lanes
-#pragma unroll 4
-    for (int i = threadIdx.x; i < L * kQuads; i += X::kThreads) {
-      const int t = i / kQuads, c = (i % kQuads) * 4;
-      float4 e = make_float4(0.f, 0.f, 0.f, 0.f), d = e, v = e;
-      const int64_t at = (t0 + t) * v_row + int64_t(h) * N + c;
-      if (t < len) {
-        e = *reinterpret_cast<const float4*>(b.e + at);
-        d = *reinterpret_cast<const float4*>(b.du + at);
-        v = load4(static_cast<const T*>(a.v) + at);
-      }
+#pragma unroll
+    for (int x = 0; x < kTok; ++x) {
+      const int i = threadIdx.x + x * X::kThreads, t = i / kQuads, c = (i % kQuads) * 4;
+      const float4 e = er[x], d = dr[x], v = vr[x];
       const float be = F.beta[t];
       float s = fmaf(e.x, d.x, fmaf(e.y, d.y, fmaf(e.z, d.z, e.w * d.w)));
       float w = fmaf(v.x, d.x, fmaf(v.y, d.y, fmaf(v.z, d.z, v.w * d.w)));
@@ -551,51 +580,50 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
       put_parts<PP, X::kTile>(smem + X::kOffDe + to,
                               make_float4(be * d.x, be * d.y, be * d.z, be * d.w));
     }
-    // 64 rows of a state into parts
-    auto load_state = [&](const float* src, int r0, auto parts) {
-#pragma unroll 4
-      for (int i = threadIdx.x; i < X::kRows * kQuads; i += X::kThreads) {
-        const int r = i / kQuads, c = (i % kQuads) * 4;
-        put_parts<decltype(parts)::value, X::kState>(smem + X::kOffS + (r * X::kPitch + c) * 2,
-                                 *reinterpret_cast<const float4*>(src + (r0 + r) * N + c));
-      }
-    };
     const uint32_t rows = at_rows(lane, X::kPitch) + uint32_t(strip * 16 * X::kPitch) * 2u;
     const uint32_t cols = at_channels(lane, X::kPitch) + uint32_t(slice * X::kCols) * 2u;
     float q1[NT][4], k1[NT][4], k2[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) zero(q1[n]), zero(k1[n]), zero(k2[n]);
-    // S^T dy, S^T de
+    // S^T dy, S^T de; while a block of rows is at work the next is fetched
 #pragma unroll 1
     for (int r0 = 0; r0 < N; r0 += X::kRows) {
       if (r0 > 0) __syncthreads();
-      load_state(b.checkpoints + state_at, r0, std::integral_constant<int, PA>());
+      store_state(std::integral_constant<int, PA>());
       cp_async_wait_all();
       __syncthreads();
-      product<PI, PA, NT, X::kRows, false, true, true>(q1, sb + X::kOffDy + rows + r0 * 2, X::kTile,
-                                                       X::kPitch, sb + X::kOffS + cols, X::kState,
-                                                       X::kPitch);
-      product<PP, PP, NT, X::kRows, false, true, kExact>(
-          k1, sb + X::kOffDe + rows + r0 * 2, X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
-          X::kPitch);
+      if (r0 + X::kRows < N)
+        fetch_state(b.checkpoints + state_at, r0 + X::kRows);
+      else
+        fetch_state(b.dstates + state_at, 0);
+      product<PI, PA, NT, false, true, true>(q1, 0, X::kRows, sb + X::kOffDy + rows + r0 * 2,
+                                             X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
+                                             X::kPitch);
+      product<PP, PP, NT, false, true, kExact>(k1, 0, X::kRows, sb + X::kOffDe + rows + r0 * 2,
+                                               X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
+                                               X::kPitch);
     }
     // dD^T u, and <dD, S_L>
     float inner = 0.f;
     const int64_t next_at = state_at + int64_t(a.H) * N * N;
 #pragma unroll 1
     for (int r0 = 0; r0 < N; r0 += X::kRows) {
+      float4 nr[kSt];
+#pragma unroll
+      for (int x = 0; x < kSt; ++x)
+        nr[x] = reinterpret_cast<const float4*>(b.checkpoints + next_at +
+                                                r0 * N)[threadIdx.x + x * X::kThreads];
       __syncthreads();
-      load_state(b.dstates + state_at, r0, std::integral_constant<int, PP>());
-#pragma unroll 4
-      for (int i = threadIdx.x; i < X::kRows * kQuads; i += X::kThreads) {
-        const float4 x = reinterpret_cast<const float4*>(b.dstates + state_at + r0 * N)[i];
-        const float4 y = reinterpret_cast<const float4*>(b.checkpoints + next_at + r0 * N)[i];
-        inner = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, inner))));
-      }
+      store_state(std::integral_constant<int, PP>());
+#pragma unroll
+      for (int x = 0; x < kSt; ++x)
+        inner = fmaf(sr[x].x, nr[x].x, fmaf(sr[x].y, nr[x].y,
+                     fmaf(sr[x].z, nr[x].z, fmaf(sr[x].w, nr[x].w, inner))));
       __syncthreads();
-      product<PP, PP, NT, X::kRows, false, true, kExact>(
-          k2, sb + X::kOffU + rows + r0 * 2, X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
-          X::kPitch);
+      if (r0 + X::kRows < N) fetch_state(b.dstates + state_at, r0 + X::kRows);
+      product<PP, PP, NT, false, true, kExact>(k2, 0, X::kRows, sb + X::kOffU + rows + r0 * 2,
+                                               X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
+                                               X::kPitch);
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, m);
@@ -622,19 +650,22 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
 #pragma unroll
     for (int n = 0; n < NW; ++n) zero(pw[n]), zero(zw[n]);
     const int j0 = slice * (L / kShares);
-    if (shares) {
+    // (16 x 16 blocks above the diagonal are neither made nor read)
+    const int tiles = shares ? (strip + 1) * 2 - j0 / 8 : 0;
+    if (tiles > 0) {
       const uint32_t us =
           sb + X::kOffU + at_tokens(lane, X::kPitch) + uint32_t(j0 * X::kPitch) * 2u;
-      product<PI, PA, NW, N, false, false, true>(pw, sb + X::kOffDy + rows, X::kTile, X::kPitch, us,
-                                                 X::kTile, X::kPitch);
-      product<PP, PP, NW, N, false, false, kExact>(zw, sb + X::kOffDe + rows, X::kTile, X::kPitch,
-                                                   us, X::kTile, X::kPitch);
+      product<PI, PA, NW, false, false, true>(pw, 0, N, sb + X::kOffDy + rows, X::kTile, X::kPitch,
+                                              us, X::kTile, X::kPitch, tiles);
+      product<PP, PP, NW, false, false, kExact>(zw, 0, N, sb + X::kOffDe + rows, X::kTile,
+                                                X::kPitch, us, X::kTile, X::kPitch, tiles);
     }
     __syncthreads();  // dD's rows and de have been read: P and Z take their places
 #pragma unroll
-    for (int n = 0; n < (shares ? NW : 0); ++n)
+    for (int n = 0; n < NW; ++n)
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
+        if (n >= tiles) continue;
         const int i = strip * 16 + g4 + z * 8, j = j0 + n * 8 + 2 * t4;
         const Decay ci = F.c[i];
         const float d0 = i >= j ? decay_between(ci, F.c[j]) : 0.f;
@@ -655,14 +686,15 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads)
     // dq: + P K; k2: + P^T Q; k1: + Z K + Z^T K
     const uint32_t prow = at_rows(lane, X::kPPitch) + uint32_t(strip * 16 * X::kPPitch) * 2u;
     const uint32_t pcol = at_tokens(lane, X::kPPitch) + uint32_t(strip * 16) * 2u;
-    product<PA, PI, NT, L, false, true, true>(q1, sb + X::kOffS + prow, X::kPTile, X::kPPitch,
-                                              sb + X::kOffK + cols, X::kTile, X::kPitch);
-    product<PP, PI, NT, L, true, true, kExact>(k2, sb + X::kOffS + pcol, X::kPTile, X::kPPitch,
-                                               sb + X::kOffQ + cols, X::kTile, X::kPitch);
-    product<PP, PI, NT, L, false, true, kExact>(k1, sb + X::kOffDe + prow, X::kPTile, X::kPPitch,
-                                                sb + X::kOffK + cols, X::kTile, X::kPitch);
-    product<PP, PI, NT, L, true, true, kExact>(k1, sb + X::kOffDe + pcol, X::kPTile, X::kPPitch,
-                                               sb + X::kOffK + cols, X::kTile, X::kPitch);
+    const int below = strip * 16, upto = strip * 16 + 16;
+    product<PA, PI, NT, false, true, true>(q1, 0, upto, sb + X::kOffS + prow, X::kPTile, X::kPPitch,
+                                           sb + X::kOffK + cols, X::kTile, X::kPitch);
+    product<PP, PI, NT, true, true, kExact>(k2, below, L, sb + X::kOffS + pcol, X::kPTile,
+                                            X::kPPitch, sb + X::kOffQ + cols, X::kTile, X::kPitch);
+    product<PP, PI, NT, false, true, kExact>(k1, 0, upto, sb + X::kOffDe + prow, X::kPTile,
+                                             X::kPPitch, sb + X::kOffK + cols, X::kTile, X::kPitch);
+    product<PP, PI, NT, true, true, kExact>(k1, below, L, sb + X::kOffDe + pcol, X::kPTile,
+                                            X::kPPitch, sb + X::kOffK + cols, X::kTile, X::kPitch);
     float read[2];
     dot_rows(q1, X::kOffQ, read);
     if (t4 == 0) {
