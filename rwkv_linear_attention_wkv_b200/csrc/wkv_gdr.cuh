@@ -92,6 +92,14 @@ __device__ __forceinline__ void split_tiles(const float (&t0)[4], const float (&
 
 __device__ __forceinline__ void zero(float (&c)[4]) { c[0] = c[1] = c[2] = c[3] = 0.f; }
 
+// s = c s + d, two at a time.
+__device__ __forceinline__ void scale_add(float (&s)[4], float c, const float (&d)[4]) {
+  const float2 cc = make_float2(c, c);
+  const float2 lo = __ffma2_rn(cc, make_float2(s[0], s[1]), make_float2(d[0], d[1]));
+  const float2 hi = __ffma2_rn(cc, make_float2(s[2], s[3]), make_float2(d[2], d[3]));
+  s[0] = lo.x; s[1] = lo.y; s[2] = hi.x; s[3] = hi.y;
+}
+
 // The part pairs of a product, largest first: P operand parts of b (1: exact bf16, 3: split).
 // FULL leaves out none of the six (three with P = 1) that fp32 accuracy takes; without it the
 // pairs below 2^-16 go.
@@ -219,64 +227,61 @@ __device__ __forceinline__ Decay decay_sums(float g, int lane) {
 }
 
 // The strictly lower part of (I + L)^-1 for a strictly lower 16 x 16 L in shared memory (pitch
-// 20), left in the same place. The two diagonal 8 x 8 blocks A and B by forward substitution,
-// one column a lane; the block below them is -B^-1 (L21 A^-1). `tmp`: 8 x 8 floats.
+// 20), left in the same place. The two diagonal 8 x 8 blocks A and B by forward substitution, one
+// column a lane; the block below them is -B^-1 (L21 A^-1). `tmp`: 8 x 8 floats.
 constexpr int kLP = 20;
 constexpr int kLTmp = 64;
 __device__ __forceinline__ void invert_group(float* L, float* tmp, int lane) {
   const int b = (lane >> 3) & 1, c = lane & 7;
   const float* const D = L + b * 8 * (kLP + 1);
   __syncwarp();
-  float4 r[8][2];
+  float r[8][8];
 #pragma unroll
   for (int i = 1; i < 8; ++i) {
-    r[i][0] = *reinterpret_cast<const float4*>(D + i * kLP);
-    if (i > 4) r[i][1] = *reinterpret_cast<const float4*>(D + i * kLP + 4);
+    const float4 lo = *reinterpret_cast<const float4*>(D + i * kLP);
+    r[i][0] = lo.x; r[i][1] = lo.y; r[i][2] = lo.z; r[i][3] = lo.w;
+    if (i > 4) {
+      const float4 hi = *reinterpret_cast<const float4*>(D + i * kLP + 4);
+      r[i][4] = hi.x; r[i][5] = hi.y; r[i][6] = hi.z; r[i][7] = hi.w;
+    }
   }
   float x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float* l = reinterpret_cast<const float*>(r[i]);
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int j = 0; j < i; ++j) (j & 1 ? s1 : s0) = fmaf(l[j], x[j], j & 1 ? s1 : s0);
+    for (int j = 0; j < i; ++j) {
+      if (j & 1)
+        s1 = fmaf(r[i][j], x[j], s1);
+      else
+        s0 = fmaf(r[i][j], x[j], s0);
+    }
     x[i] = i < c ? 0.f : i == c ? 1.f : -(s0 + s1);
   }
   __syncwarp();
-  // rows of A^-1 and B^-1 with their unit diagonals
-  if (lane < 16) {
+  // A^-1 and B^-1 with their unit diagonals
+  if (lane < kG) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) L[(b * 8 + i) * kLP + b * 8 + c] = x[i];
   }
   __syncwarp();
   const int row = lane >> 2, col = (lane & 3) * 2;
-  {
-    const float4 l0 = *reinterpret_cast<const float4*>(L + (8 + row) * kLP);
-    const float4 l1 = *reinterpret_cast<const float4*>(L + (8 + row) * kLP + 4);
+  auto times = [&](const float* left, const float* right, int pitch) {
+    const float4 l0 = *reinterpret_cast<const float4*>(left);
+    const float4 l1 = *reinterpret_cast<const float4*>(left + 4);
     const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
-    float t0 = 0.f, t1 = 0.f;
+    float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float2 y = *reinterpret_cast<const float2*>(L + k * kLP + col);
-      t0 = fmaf(l[k], y.x, t0);
-      t1 = fmaf(l[k], y.y, t1);
+      const float2 y = *reinterpret_cast<const float2*>(right + k * pitch + col);
+      s = make_float2(fmaf(l[k], y.x, s.x), fmaf(l[k], y.y, s.y));
     }
-    *reinterpret_cast<float2*>(tmp + row * 8 + col) = make_float2(t0, t1);
-  }
+    return s;
+  };
+  *reinterpret_cast<float2*>(tmp + row * 8 + col) = times(L + (8 + row) * kLP, L, kLP);
   __syncwarp();
-  {
-    const float4 l0 = *reinterpret_cast<const float4*>(L + (8 + row) * kLP + 8);
-    const float4 l1 = *reinterpret_cast<const float4*>(L + (8 + row) * kLP + 12);
-    const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
-    float t0 = 0.f, t1 = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 y = *reinterpret_cast<const float2*>(tmp + k * 8 + col);
-      t0 = fmaf(l[k], y.x, t0);
-      t1 = fmaf(l[k], y.y, t1);
-    }
-    *reinterpret_cast<float2*>(L + (8 + row) * kLP + col) = make_float2(-t0, -t1);
-  }
+  const float2 t = times(L + (8 + row) * kLP + 8, tmp, 8);
+  *reinterpret_cast<float2*>(L + (8 + row) * kLP + col) = make_float2(-t.x, -t.y);
   if (lane < kG) L[lane * (kLP + 1)] = 0.f;
   __syncwarp();
 }
@@ -335,14 +340,16 @@ struct GroupMats {
   float pad[3];
 };
 
-// Sizes of the two kernels that walk sequences in groups: NG producer warps, each with a group
-// of a step, and NC consumer warps of 16 value channels each. "v" is whatever comes per value
-// head: v, or dy.
-
-template <typename T, int N, int NC, int NG>
+// Sizes of the two kernels that walk sequences in groups: steps of NG groups, prepared by NP
+// producer warps (NG, or 2 NG: two a group), and NC consumer warps of 16 value channels each. "v"
+// is whatever comes per value head: v, or dy.
+template <typename T, int N, int NC, int NG, int NP>
 struct Shape {
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int kParts = kBf16 ? 1 : 3;      // operand parts of q and k
+  static constexpr int kGroups = NG, kProducers = NP;
+  static constexpr bool kPairs = NP == 2 * NG;      // of producers
+  static_assert(kPairs || (NP == NG && kBf16), "one or two producers a group");
   static constexpr int kStep = NG * kG;             // tokens of a step
   static constexpr int kPitch = N + 8;              // bf16 tiles (16-byte rows, no conflicts)
   static constexpr int kPitchF = N + 4;             // fp32 tiles
@@ -361,66 +368,40 @@ struct Shape {
   static constexpr int kOffL = kOffMats + 2 * NG * int(sizeof(GroupMats));
   static constexpr int kOffY = kOffL + NG * (kG * kLP + kLTmp) * 4;
   static constexpr int kSmem = kOffY + (kBf16 ? NC * kG * kStagePitch * 2 : 0);
-  static constexpr int kThreads = 32 * (NC + NG);
+  static constexpr int kThreads = 32 * (NC + NP);
 };
 
 
-// q, k (rows of N) and v (rows of kVRows) of a step of the sequence, by the producers.
-template <typename T, int N, class X, int NG>
-__device__ __forceinline__ void load_step(uint32_t kd, uint32_t qd, uint32_t vd, const T* k,
-                                          const T* q, const T* v, int64_t qk_row, int64_t v_row,
-                                          int first, int len, int thread) {
-  constexpr int kSize = int(sizeof(T)), kPitch = X::kBf16 ? X::kPitch * 2 : X::kPitchF * 4;
-  const int left = len - first;
-  load_tile<X::kStep, N * kSize, kPitch, NG * 32>(kd, k + first * qk_row, qk_row * kSize, left,
-                                                  thread);
-  load_tile<X::kStep, N * kSize, kPitch, NG * 32>(qd, q + first * qk_row, qk_row * kSize, left,
-                                                  thread);
-  load_tile<X::kStep, X::kVRows * kSize, X::kVPitch * kSize, NG * 32>(
-      vd, v + first * v_row, v_row * kSize, left, thread);
-}
-
-// Two products over the channels of a group's tokens at byte offset `off` of every part's tile:
-// kk = K K^T, and Q K^T (or, Q_COLUMNS, K Q^T).
-template <int N, int P, bool Q_COLUMNS, class Tile>
-__device__ __forceinline__ void group_products(float (&kk)[2][4], float (&qk)[2][4], Tile tile,
-                                               uint32_t off) {
-  float kc[2][4], qc[2][4];
+// A B^T over the channels of a group's tokens; A and B: 0 for k, 1 for q, at byte offset `off` of
+// every part's tile.
+template <int N, int P, class Tile>
+__device__ __forceinline__ void group_product(float (&c)[2][4], Tile tile, int A, int B,
+                                              uint32_t off) {
+  float corr[2][4];
 #pragma unroll
-  for (int n = 0; n < 2; ++n) zero(kk[n]), zero(qk[n]), zero(kc[n]), zero(qc[n]);
+  for (int n = 0; n < 2; ++n) zero(c[n]), zero(corr[n]);
 #pragma unroll
-  for (int c = 0; c < N; c += 16) {
-    uint32_t kb[P][4], qb[P][4], ka[3][4], qa[3][4];
+  for (int ch = 0; ch < N; ch += 16) {
+    uint32_t b[P][4], a[3][4], r[4];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      ldsm4(kb[p], tile(0, p) + off + c * 2);
-      ldsm4(qb[p], tile(1, p) + off + c * 2);
+      ldsm4(r, tile(A, p) + off + ch * 2);
       // the same four 8 x 8 blocks in the order of an a operand
-      ka[p][0] = kb[p][0]; ka[p][1] = kb[p][2]; ka[p][2] = kb[p][1]; ka[p][3] = kb[p][3];
-      qa[p][0] = qb[p][0]; qa[p][1] = qb[p][2]; qa[p][2] = qb[p][1]; qa[p][3] = qb[p][3];
+      a[p][0] = r[0]; a[p][1] = r[2]; a[p][2] = r[1]; a[p][3] = r[3];
+      ldsm4(b[p], tile(B, p) + off + ch * 2);
     }
     if constexpr (P == 1) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        mma(kk[n], ka[0], kb[0][2 * n], kb[0][2 * n + 1]);
-        if (Q_COLUMNS)
-          mma(qk[n], ka[0], qb[0][2 * n], qb[0][2 * n + 1]);
-        else
-          mma(qk[n], qa[0], kb[0][2 * n], kb[0][2 * n + 1]);
-      }
+      for (int n = 0; n < 2; ++n) mma(c[n], a[0], b[0][2 * n], b[0][2 * n + 1]);
     } else {
-      mma_pairs<P, true>(kk, kc, ka, kb);
-      if (Q_COLUMNS)
-        mma_pairs<P, true>(qk, qc, ka, qb);
-      else
-        mma_pairs<P, true>(qk, qc, qa, kb);
+      mma_pairs<P, true>(c, corr, a, b);
     }
   }
   if (P > 1) {
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) kk[n][x] += kc[n][x], qk[n][x] += qc[n][x];
+      for (int x = 0; x < 4; ++x) c[n][x] += corr[n][x];
   }
 }
 
@@ -520,6 +501,184 @@ __device__ __forceinline__ void put_state(float* to, const float (&S)[N / 8][4],
   for (int n = 0; n < N / 8; ++n) {
     *reinterpret_cast<float2*>(to + g4 * N + n * 8 + 2 * t4) = make_float2(S[n][0], S[n][1]);
     *reinterpret_cast<float2*>(to + (g4 + 8) * N + n * 8 + 2 * t4) = make_float2(S[n][2], S[n][3]);
+  }
+}
+
+// Four consumers and steps of two groups everywhere (heads of 128 are two CTAs). bf16: two
+// producers, 168 registers and two CTAs an SM where there is work for them, or four producers and
+// one CTA, which is quicker alone (us, singles / pairs: 1 x 2048 x 8 x 64: 134 / 121, 1 x 2048 x 8
+// x 128: 210 / 178) and slower where CTAs queue (8 x 4096 x 64 x 64: 821 / 937, 16 x 1024 x 32 x
+// 128: 582 / 618). fp32 splits q and k on the way, which takes four producers always (8 x 1024 x
+// 64 x 64: 496 / 388, 1 x 2048 x 8 x 64: 253 / 194).
+enum GdrWalkForm { kGdrWalkSingles, kGdrWalkPairs, kGdrWalkError };
+inline GdrWalkForm gdr_walk_form(const GdrArgs& a) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return kGdrWalkError;
+  return int64_t(a.n_seqs) * a.H * (a.N / 64) <= sms ? kGdrWalkPairs : kGdrWalkSingles;
+}
+
+// The producers' part of both kernels. Step s of a walk has the tokens from s kStep, counted from
+// the sequence's first token forwards, or (REVERSE) from its last step backwards. While the
+// consumers work on step i the producers copy step i + 2 in and prepare step i + 1: everything that
+// does not depend on the state. One barrier a step. A pair of warps shares a group where
+// X::kPairs: one makes the inverse, the other the read matrix and the vectors.
+//   forward: (I + A)^-1 - I with A_ij = D_ij (k_i . k_j) beta_j, and scale D_ij (q_i . k_j) beta_j,
+//   reverse: the transpose of (I + A')^-1 - I with A'_ij = D_ij (k_i . k_j) beta_i, and
+//            scale D_ij (q_i . k_j),
+// as operands whose columns are the tokens that the product is for.
+struct Walk {
+  int h, hk, part, len, steps;
+  int64_t t0;
+};
+
+// bf16 part p of q (which = 1) or k (0) of step s
+template <class X>
+__device__ __forceinline__ uint32_t tile_of(uint32_t sb, int s, int which, int p) {
+  if (X::kBf16) return sb + ((s % 3) * 2 + which) * X::kTile;
+  return sb + X::kOffSplit + (((s & 1) * 2 + which) * 3 + p) * X::kTile;
+}
+
+template <typename T, int N, class X, bool REVERSE>
+__device__ __forceinline__ void produce(const GdrArgs& a, const void* vals, const Walk& w,
+                                        unsigned char* smem, int pw, int lane) {
+  constexpr int P = X::kParts, NP = X::kProducers, kSize = int(sizeof(T));
+  const int group = X::kPairs ? pw >> 1 : pw;
+  const bool inverts = !X::kPairs || (pw & 1) == 0, reads = !X::kPairs || (pw & 1) == 1;
+  const uint32_t sb = smem_u32(smem);
+  const int g4 = lane >> 2, t4 = lane & 3, pt = pw * 32 + lane;
+  const int64_t qk_row = int64_t(a.Hk) * N, v_row = int64_t(a.H) * N;
+  const T* const q = static_cast<const T*>(a.q) + w.t0 * qk_row + int64_t(w.hk) * N;
+  const T* const k = static_cast<const T*>(a.k) + w.t0 * qk_row + int64_t(w.hk) * N;
+  const T* const v =
+      static_cast<const T*>(vals) + w.t0 * v_row + int64_t(w.h) * N + w.part * X::kVRows;
+  const float* const gp = a.g + w.t0 * a.H + w.h;
+  const float* const bp = a.beta + w.t0 * a.H + w.h;
+  GroupMats* const mats = reinterpret_cast<GroupMats*>(smem + X::kOffMats);  // [2][groups]
+  float* const Ls = reinterpret_cast<float*>(smem + X::kOffL);
+  float* const L = Ls + group * kG * kLP;
+  float* const tmp = Ls + X::kGroups * kG * kLP + group * kLTmp;
+  auto first_of = [&](int s) { return (REVERSE ? w.steps - 1 - s : s) * X::kStep; };
+
+  auto load = [&](int s) {
+    if (s < w.steps) {
+      const int first = first_of(s), left = w.len - first;
+      constexpr int kPitch = X::kBf16 ? X::kPitch * 2 : X::kPitchF * 4;
+      const uint32_t kd = X::kBf16 ? tile_of<X>(sb, s, 0, 0) : sb + (s & 1) * 2 * X::kTileF;
+      const uint32_t qd = X::kBf16 ? tile_of<X>(sb, s, 1, 0) : kd + X::kTileF;
+      load_tile<X::kStep, N * kSize, kPitch, NP * 32>(kd, k + first * qk_row, qk_row * kSize, left,
+                                                      pt);
+      load_tile<X::kStep, N * kSize, kPitch, NP * 32>(qd, q + first * qk_row, qk_row * kSize, left,
+                                                      pt);
+      load_tile<X::kStep, X::kVRows * kSize, X::kVPitch * kSize, NP * 32>(
+          sb + X::kOffV + (s % 3) * X::kVTile, v + first * v_row, v_row * kSize, left, pt);
+    }
+    cp_async_commit();
+  };
+  // g and beta of this lane's token of the next step
+  float g_next = 0.f, b_next = 0.f;
+  auto load_g = [&](int s) {
+    const int tok = first_of(s) + group * kG + (lane & 15);
+    const bool ok = s < w.steps && tok < w.len;
+    g_next = ok ? gp[int64_t(tok) * a.H] : 0.f;
+    b_next = ok ? bp[int64_t(tok) * a.H] : 0.f;
+  };
+
+  load(0);
+  load_g(0);
+  load(1);
+  for (int i = -1; i < w.steps; ++i) {
+    const int s = i + 1;  // the step to prepare
+    if (i >= 0) load(i + 2);
+    if (s < w.steps) {
+      const float gv = g_next, bv = b_next;
+      load_g(s + 1);
+      cp_async_wait<1>();
+      asm volatile("bar.sync 1, %0;" ::"n"(NP * 32) : "memory");
+      if (!X::kBf16) {
+        // the group's k (one warp) and q (the other) into three parts
+        const int which = pw & 1, row = group * kG;
+        split_tokens<N, X::kTile>(
+            reinterpret_cast<const float*>(smem + ((s & 1) * 2 + which) * X::kTileF) +
+                row * X::kPitchF,
+            smem + (tile_of<X>(sb, s, which, 0) - sb) + row * X::kPitch * 2, lane);
+        asm volatile("bar.sync 1, %0;" ::"n"(NP * 32) : "memory");
+      }
+      auto tile = [&](int which, int p) { return tile_of<X>(sb, s, which, p); };
+      const uint32_t off =
+          at_tokens(lane, X::kPitch) + uint32_t(group * kG * X::kPitch) * 2u;
+      const Decay cs = decay_sums<kG>(gv, lane);
+      const Decay cr[2] = {shfl(cs, g4), shfl(cs, g4 + 8)};
+      GroupMats& m = mats[(s & 1) * X::kGroups + group];
+      if (inverts) {
+        float kk[2][4];
+        group_product<N, P>(kk, tile, 0, 0, off);
+        const float br[2] = {__shfl_sync(0xffffffffu, bv, g4),
+                             __shfl_sync(0xffffffffu, bv, g4 + 8)};
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int col = n * 8 + 2 * t4 + y;
+            const Decay cc = shfl(cs, col);
+            const float bc = __shfl_sync(0xffffffffu, bv, col);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const float d = decay_between(cr[z], cc) * (REVERSE ? br[z] : bc);
+              kk[n][2 * z + y] = g4 + z * 8 > col ? d * kk[n][2 * z + y] : 0.f;
+            }
+          }
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            *reinterpret_cast<float2*>(L + (g4 + z * 8) * kLP + n * 8 + 2 * t4) =
+                make_float2(kk[n][2 * z], kk[n][2 * z + 1]);
+        }
+        invert_group(L, tmp, lane);
+        // operand entry (contraction j or j + 1, column i): the inverse's (i, j), or (j, i)
+        auto pair = [&](int i, int j) {
+          return REVERSE ? make_float2(L[j * kLP + i], L[(j + 1) * kLP + i])
+                         : *reinterpret_cast<const float2*>(L + i * kLP + j);
+        };
+        put_fragment<3>(m.inv, pair(g4, 2 * t4), pair(g4, 8 + 2 * t4), pair(g4 + 8, 2 * t4),
+                        pair(g4 + 8, 8 + 2 * t4), lane);
+        __syncwarp();
+      }
+      if (reads) {
+        // q_i . k_j, rows i; reverse: rows j
+        float qk[2][4];
+        group_product<N, P>(qk, tile, REVERSE ? 0 : 1, REVERSE ? 1 : 0, off);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int col = n * 8 + 2 * t4 + y;
+            const Decay cc = shfl(cs, col);
+            const float bc = REVERSE ? 1.f : __shfl_sync(0xffffffffu, bv, col);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int row = g4 + z * 8, x = 2 * z + y;
+              const float d =
+                  REVERSE ? col >= row ? decay_between(cc, cr[z]) : 0.f
+                          : row >= col ? decay_between(cr[z], cc) * bc : 0.f;
+              qk[n][x] = a.scale * (d * qk[n][x]);
+            }
+          }
+        auto two = [](const float(&t)[4], int j) { return make_float2(t[j], t[j + 1]); };
+        put_fragment<!REVERSE && X::kBf16 ? 2 : 3>(m.read, two(qk[0], 0), two(qk[1], 0),
+                                                   two(qk[0], 2), two(qk[1], 2), lane);
+        const Decay last = shfl(cs, 15);
+        if (lane < kG) {
+          const float d = ex2(cs.hi + cs.lo), to_end = decay_between(last, cs);
+          m.decay[lane] = d;
+          m.out[lane] = a.scale * d;
+          m.write[lane] = REVERSE ? to_end : to_end * bv;
+          if (REVERSE) m.beta[lane] = bv;
+          if (lane == 15) m.end = d;
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 

@@ -41,16 +41,16 @@ __device__ __forceinline__ void mma_exact_a(float (&c)[2][4], const uint32_t (&a
     for (int n = 0; n < 2; ++n) mma(c[n], a, b[p][2 * n], b[p][2 * n + 1]);
 }
 
-template <typename T, int N, int NC, int NG, int CTAS>
-__global__ void __launch_bounds__(Shape<T, N, NC, NG>::kThreads, CTAS)
+template <typename T, int N, int NC, int NG, int NP, int CTAS>
+__global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
     gdr_chain_kernel(GdrBwdArgs b) {
-  using X = Shape<T, N, NC, NG>;
+  using X = Shape<T, N, NC, NG, NP>;
   constexpr int P = X::kParts;
   extern __shared__ __align__(128) unsigned char smem[];
   const GdrArgs& a = b.p;
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g4 = lane >> 2, t4 = lane & 3;
+  const int t4 = lane & 3;
   constexpr int kSplitRows = N / X::kVRows;
   const int part = blockIdx.x % kSplitRows;
   const int sh = blockIdx.x / kSplitRows;
@@ -59,115 +59,14 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG>::kThreads, CTAS)
   const int64_t t0 = sequence(a, seq, len);
   const int steps = (len + X::kStep - 1) / X::kStep;
   GroupMats* const mats = reinterpret_cast<GroupMats*>(smem + X::kOffMats);  // [2][NG]
-  const int64_t qk_row = int64_t(a.Hk) * N, v_row = int64_t(a.H) * N;
+  const int64_t v_row = int64_t(a.H) * N;
 
   // Steps are counted in the order they are taken: step i has the tokens from `first_of(i)`.
   auto first_of = [&](int i) { return (steps - 1 - i) * X::kStep; };
-  auto tile = [&](int s, int which, int p) -> uint32_t {
-    if (X::kBf16) return sb + ((s % 3) * 2 + which) * X::kTile;
-    return sb + X::kOffSplit + (((s & 1) * 2 + which) * 3 + p) * X::kTile;
-  };
+  auto tile = [&](int s, int which, int p) { return tile_of<X>(sb, s, which, p); };
 
   if (warp >= NC) {
-    // ------------------------------------------------------------------ producers
-    const int pw = warp - NC, pt = pw * 32 + lane;
-    const T* q = static_cast<const T*>(a.q) + t0 * qk_row + int64_t(hk) * N;
-    const T* k = static_cast<const T*>(a.k) + t0 * qk_row + int64_t(hk) * N;
-    const T* dy = static_cast<const T*>(b.dy) + t0 * v_row + int64_t(h) * N + part * X::kVRows;
-    const float* gp = a.g + t0 * a.H + h;
-    const float* bp = a.beta + t0 * a.H + h;
-    float* const L = reinterpret_cast<float*>(smem + X::kOffL) + pw * kG * kLP;
-    float* const tmp = reinterpret_cast<float*>(smem + X::kOffL) + NG * kG * kLP + pw * kLTmp;
-
-    auto load = [&](int s) {
-      if (s < steps)
-        load_step<T, N, X, NG>(X::kBf16 ? tile(s, 0, 0) : sb + ((s & 1) * 2 + 0) * X::kTileF,
-                               X::kBf16 ? tile(s, 1, 0) : sb + ((s & 1) * 2 + 1) * X::kTileF,
-                               sb + X::kOffV + (s % 3) * X::kVTile, k, q, dy, qk_row, v_row,
-                               first_of(s), len, pt);
-      cp_async_commit();
-    };
-    float g_next = 0.f, b_next = 0.f;
-    auto load_g = [&](int s) {
-      const int tok = first_of(s) + pw * kG + (lane & 15);
-      const bool ok = s < steps && tok < len;
-      g_next = ok ? gp[int64_t(tok) * a.H] : 0.f;
-      b_next = ok ? bp[int64_t(tok) * a.H] : 0.f;
-    };
-    auto sync_producers = [&] {
-      if (NG == 1)
-        __syncwarp();
-      else
-        asm volatile("bar.sync 1, %0;" ::"n"(NG * 32) : "memory");
-    };
-
-    load(0);
-    load_g(0);
-    load(1);
-    for (int i = -1; i < steps; ++i) {
-      const int s = i + 1;  // the step to prepare
-      if (i >= 0) load(i + 2);
-      if (s < steps) {
-        const float gv = g_next, bv = b_next;
-        load_g(s + 1);
-        cp_async_wait<1>();
-        sync_producers();
-        if (!X::kBf16) {
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            split_tokens<N, X::kTile>(
-                reinterpret_cast<const float*>(smem + ((s & 1) * 2 + w) * X::kTileF) +
-                    pw * kG * X::kPitchF,
-                smem + (tile(s, w, 0) - sb) + pw * kG * X::kPitch * 2, lane);
-          __syncwarp();
-        }
-        // k_i . k_j (rows i) and k_j . q_i (rows j)
-        float kk[2][4], kq[2][4];
-        group_products<N, P, true>(
-            kk, kq, [&](int w, int p) { return tile(s, w, p); },
-            at_tokens(lane, X::kPitch) + uint32_t(pw * kG * X::kPitch) * 2u);
-        const Decay cs = decay_sums<kG>(gv, lane);
-        GroupMats& m = mats[(s & 1) * NG + pw];
-        float read[2][4];
-        const Decay cr[2] = {shfl(cs, g4), shfl(cs, g4 + 8)};
-        const float br[2] = {__shfl_sync(0xffffffffu, bv, g4),
-                             __shfl_sync(0xffffffffu, bv, g4 + 8)};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int col = n * 8 + 2 * t4 + y;
-            const Decay cc = shfl(cs, col);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const int row = g4 + z * 8, x = 2 * z + y;
-              L[row * kLP + col] =
-                  row > col ? decay_between(cr[z], cc) * br[z] * kk[n][x] : 0.f;
-              read[n][x] = col >= row ? a.scale * (decay_between(cc, cr[z]) * kq[n][x]) : 0.f;
-            }
-          }
-        auto two = [](const float(&t)[4], int i) { return make_float2(t[i], t[i + 1]); };
-        put_fragment<3>(m.read, two(read[0], 0), two(read[1], 0), two(read[0], 2), two(read[1], 2),
-                        lane);
-        invert_group(L, tmp, lane);
-        // the transposed inverse: entry (i, j) multiplies R_i into du_j
-        auto down = [&](int i, int j) {
-          return make_float2(L[i * kLP + j], L[(i + 1) * kLP + j]);
-        };
-        put_fragment<3>(m.inv, down(2 * t4, g4), down(8 + 2 * t4, g4), down(2 * t4, g4 + 8),
-                        down(8 + 2 * t4, g4 + 8), lane);
-        const Decay last = shfl(cs, 15);
-        if (lane < kG) {
-          const float d = ex2(cs.hi + cs.lo);
-          m.decay[lane] = d;
-          m.out[lane] = a.scale * d;
-          m.write[lane] = decay_between(last, cs);
-          m.beta[lane] = bv;
-          if (lane == 15) m.end = d;
-        }
-      }
-      __syncthreads();
-    }
+    produce<T, N, X, true>(a, b.dy, {h, hk, part, len, steps, t0}, smem, warp - NC, lane);
     return;
   }
 
@@ -270,9 +169,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG>::kThreads, CTAS)
         mma_up<P, true>(d, ap, qb);
         mma_up<P, true>(d, bp, kb);
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) S[c / 8 + n][x] = fmaf(end, S[c / 8 + n][x], d[n][x]);
+        for (int n = 0; n < 2; ++n) scale_add(S[c / 8 + n], end, d[n]);
       }
       put_tokens<float>(du + first * v_row, v_row, r, len - first, nullptr, lane);
       put_tokens<T>(dv + first * v_row, v_row, de, len - first, stage, lane);
@@ -759,11 +656,11 @@ bool allow_smem(K* kernel, int bytes) {
          cudaSuccess;
 }
 
-template <typename T, int N, int NC, int NG, int CTAS>
+template <typename T, int N, int NC, int NG, int NP, int CTAS>
 int launch(const GdrBwdArgs& b, cudaStream_t stream) {
-  using X = Shape<T, N, NC, NG>;
+  using X = Shape<T, N, NC, NG, NP>;
   using Y = Chunk<T, N>;
-  auto* chain = gdr_chain_kernel<T, N, NC, NG, CTAS>;
+  auto* chain = gdr_chain_kernel<T, N, NC, NG, NP, CTAS>;
   auto* rest = gdr_chunk_kernel<T, N>;
   if (!allow_smem(chain, X::kSmem) || !allow_smem(rest, Y::kSmem)) return WKV_ERR_CUDA;
   const unsigned grid = unsigned(int64_t(b.p.n_seqs) * b.p.H * (N / X::kVRows));
@@ -776,11 +673,19 @@ int launch(const GdrBwdArgs& b, cudaStream_t stream) {
 }  // namespace
 
 int launch_gdr_backward(const GdrBwdArgs& b, cudaStream_t stream) {
-  if (b.p.bf16)
-    return b.p.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 2>(b, stream)
-                       : launch<__nv_bfloat16, 128, 4, 2, 2>(b, stream);
-  return b.p.N == 64 ? launch<float, 64, 4, 2, 1>(b, stream)
-                     : launch<float, 128, 4, 2, 1>(b, stream);
+  if (!b.p.bf16)
+    return b.p.N == 64 ? launch<float, 64, 4, 2, 4, 1>(b, stream)
+                     : launch<float, 128, 4, 2, 4, 1>(b, stream);
+  switch (gdr_walk_form(b.p)) {
+    case kGdrWalkPairs:
+      return b.p.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 4, 1>(b, stream)
+                       : launch<__nv_bfloat16, 128, 4, 2, 4, 1>(b, stream);
+    case kGdrWalkSingles:
+      return b.p.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 2, 2>(b, stream)
+                       : launch<__nv_bfloat16, 128, 4, 2, 2, 2>(b, stream);
+    default:
+      return WKV_ERR_CUDA;
+  }
 }
 
 }  // namespace wkv

@@ -23,15 +23,15 @@ using namespace gdr;
 
 namespace {
 
-template <typename T, int N, int NC, int NG, int CTAS>
-__global__ void __launch_bounds__(Shape<T, N, NC, NG>::kThreads, CTAS)
+template <typename T, int N, int NC, int NG, int NP, int CTAS>
+__global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
     gdr_fwd_kernel(GdrArgs a, float* e_out, float* checkpoints) {
-  using X = Shape<T, N, NC, NG>;
+  using X = Shape<T, N, NC, NG, NP>;
   constexpr int P = X::kParts;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g4 = lane >> 2, t4 = lane & 3;
+  const int t4 = lane & 3;
   constexpr int kSplitRows = N / X::kVRows;
   const int part = blockIdx.x % kSplitRows;
   const int sh = blockIdx.x / kSplitRows;
@@ -39,112 +39,13 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG>::kThreads, CTAS)
   int len;
   const int64_t t0 = sequence(a, seq, len);
   const int steps = (len + X::kStep - 1) / X::kStep;
-  GroupMats* const mats = reinterpret_cast<GroupMats*>(smem + X::kOffMats);  // [2][NG]
-  const int64_t qk_row = int64_t(a.Hk) * N, v_row = int64_t(a.H) * N;
+  const GroupMats* const mats = reinterpret_cast<GroupMats*>(smem + X::kOffMats);  // [2][NG]
+  const int64_t v_row = int64_t(a.H) * N;
 
-  // bf16 part p of q (which = 1) or k (0) of step s
-  auto tile = [&](int s, int which, int p) -> uint32_t {
-    if (X::kBf16) return sb + ((s % 3) * 2 + which) * X::kTile;
-    return sb + X::kOffSplit + (((s & 1) * 2 + which) * 3 + p) * X::kTile;
-  };
+  auto tile = [&](int s, int which, int p) { return tile_of<X>(sb, s, which, p); };
 
   if (warp >= NC) {
-    // ------------------------------------------------------------------ producers
-    const int pw = warp - NC, pt = pw * 32 + lane;
-    const T* q = static_cast<const T*>(a.q) + t0 * qk_row + int64_t(hk) * N;
-    const T* k = static_cast<const T*>(a.k) + t0 * qk_row + int64_t(hk) * N;
-    const T* v = static_cast<const T*>(a.v) + t0 * v_row + int64_t(h) * N + part * X::kVRows;
-    const float* gp = a.g + t0 * a.H + h;
-    const float* bp = a.beta + t0 * a.H + h;
-    float* const L = reinterpret_cast<float*>(smem + X::kOffL) + pw * kG * kLP;
-    float* const tmp = reinterpret_cast<float*>(smem + X::kOffL) + NG * kG * kLP + pw * kLTmp;
-
-    auto load = [&](int s) {
-      if (s < steps)
-        load_step<T, N, X, NG>(X::kBf16 ? tile(s, 0, 0) : sb + ((s & 1) * 2 + 0) * X::kTileF,
-                               X::kBf16 ? tile(s, 1, 0) : sb + ((s & 1) * 2 + 1) * X::kTileF,
-                               sb + X::kOffV + (s % 3) * X::kVTile, k, q, v, qk_row, v_row,
-                               s * X::kStep, len, pt);
-      cp_async_commit();
-    };
-    // g and beta of this lane's token of step s
-    float g_next = 0.f, b_next = 0.f;
-    auto load_g = [&](int s) {
-      const int tok = s * X::kStep + pw * kG + (lane & 15);
-      g_next = tok < len ? gp[int64_t(tok) * a.H] : 0.f;
-      b_next = tok < len ? bp[int64_t(tok) * a.H] : 0.f;
-    };
-    auto sync_producers = [&] {
-      if (NG == 1)
-        __syncwarp();
-      else
-        asm volatile("bar.sync 1, %0;" ::"n"(NG * 32) : "memory");
-    };
-
-    load(0);
-    load_g(0);
-    load(1);
-    for (int i = -1; i < steps; ++i) {
-      const int s = i + 1;  // the step to prepare
-      if (i >= 0) load(i + 2);
-      if (s < steps) {
-        const float gv = g_next, bv = b_next;
-        load_g(s + 1);
-        cp_async_wait<1>();
-        sync_producers();
-        if (!X::kBf16) {
-          // this warp's 16 tokens of q and k into three parts
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            split_tokens<N, X::kTile>(
-                reinterpret_cast<const float*>(smem + ((s & 1) * 2 + w) * X::kTileF) +
-                    pw * kG * X::kPitchF,
-                smem + (tile(s, w, 0) - sb) + pw * kG * X::kPitch * 2, lane);
-          __syncwarp();
-        }
-        float kk[2][4], qk[2][4];
-        group_products<N, P, false>(
-            kk, qk, [&](int w, int p) { return tile(s, w, p); },
-            at_tokens(lane, X::kPitch) + uint32_t(pw * kG * X::kPitch) * 2u);
-        // decays between tokens, the two matrices
-        const Decay cs = decay_sums<kG>(gv, lane);
-        GroupMats& m = mats[(s & 1) * NG + pw];
-        float read[2][4];
-        const Decay ci[2] = {shfl(cs, g4), shfl(cs, g4 + 8)};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int col = n * 8 + 2 * t4 + y;
-            const Decay cj = shfl(cs, col);
-            const float bj = __shfl_sync(0xffffffffu, bv, col);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const int row = g4 + z * 8, x = 2 * z + y;
-              const float d = row >= col ? decay_between(ci[z], cj) * bj : 0.f;
-              read[n][x] = a.scale * (d * qk[n][x]);
-              L[row * kLP + col] = row > col ? d * kk[n][x] : 0.f;
-            }
-          }
-        // columns of the product are the rows (i) of the read matrix
-        auto two = [](const float(&t)[4], int i) { return make_float2(t[i], t[i + 1]); };
-        put_fragment<X::kBf16 ? 2 : 3>(m.read, two(read[0], 0), two(read[1], 0), two(read[0], 2),
-                                       two(read[1], 2), lane);
-        invert_group(L, tmp, lane);
-        auto pair = [&](int i, int j) { return *reinterpret_cast<const float2*>(L + i * kLP + j); };
-        put_fragment<3>(m.inv, pair(g4, 2 * t4), pair(g4, 8 + 2 * t4), pair(g4 + 8, 2 * t4),
-                        pair(g4 + 8, 8 + 2 * t4), lane);
-        const Decay last = shfl(cs, 15);
-        if (lane < kG) {
-          const float d = ex2(cs.hi + cs.lo);
-          m.decay[lane] = d;
-          m.out[lane] = a.scale * d;
-          m.write[lane] = decay_between(last, cs) * bv;
-          if (lane == 15) m.end = d;
-        }
-      }
-      __syncthreads();
-    }
+    produce<T, N, X, false>(a, a.v, {h, hk, part, len, steps, t0}, smem, warp - NC, lane);
     return;
   }
 
@@ -246,9 +147,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG>::kThreads, CTAS)
         zero(d[1]);
         mma_up<P, true>(d, wp, kb);
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) S[c / 8 + n][x] = fmaf(end, S[c / 8 + n][x], d[n][x]);
+        for (int n = 0; n < 2; ++n) scale_add(S[c / 8 + n], end, d[n]);
       }
       if (eo != nullptr) put_tokens<float>(eo + first * v_row, v_row, e, len - first, nullptr, lane);
       put_tokens<T>(y + first * v_row, v_row, o, len - first, stage, lane);
@@ -264,10 +163,10 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG>::kThreads, CTAS)
   if (a.s1 != nullptr) put_state<N>(a.s1 + state_at, S, lane);
 }
 
-template <typename T, int N, int NC, int NG, int CTAS>
+template <typename T, int N, int NC, int NG, int NP, int CTAS>
 int launch(const GdrArgs& a, float* e, float* checkpoints, cudaStream_t stream) {
-  using X = Shape<T, N, NC, NG>;
-  auto* kernel = gdr_fwd_kernel<T, N, NC, NG, CTAS>;
+  using X = Shape<T, N, NC, NG, NP>;
+  auto* kernel = gdr_fwd_kernel<T, N, NC, NG, NP, CTAS>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, X::kSmem) !=
       cudaSuccess)
     return WKV_ERR_CUDA;
@@ -279,12 +178,19 @@ int launch(const GdrArgs& a, float* e, float* checkpoints, cudaStream_t stream) 
 }  // namespace
 
 int launch_gdr_chunked(const GdrArgs& a, float* e, float* checkpoints, cudaStream_t stream) {
-  // Four consumers and two producers everywhere; 128 rows are two CTAs.
-  if (a.bf16)
-    return a.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 2>(a, e, checkpoints, stream)
-                     : launch<__nv_bfloat16, 128, 4, 2, 2>(a, e, checkpoints, stream);
-  return a.N == 64 ? launch<float, 64, 4, 2, 1>(a, e, checkpoints, stream)
-                   : launch<float, 128, 4, 2, 1>(a, e, checkpoints, stream);
+  if (!a.bf16)
+    return a.N == 64 ? launch<float, 64, 4, 2, 4, 1>(a, e, checkpoints, stream)
+                     : launch<float, 128, 4, 2, 4, 1>(a, e, checkpoints, stream);
+  switch (gdr_walk_form(a)) {
+    case kGdrWalkPairs:
+      return a.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 4, 1>(a, e, checkpoints, stream)
+                       : launch<__nv_bfloat16, 128, 4, 2, 4, 1>(a, e, checkpoints, stream);
+    case kGdrWalkSingles:
+      return a.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 2, 2>(a, e, checkpoints, stream)
+                       : launch<__nv_bfloat16, 128, 4, 2, 2, 2>(a, e, checkpoints, stream);
+    default:
+      return WKV_ERR_CUDA;
+  }
 }
 
 }  // namespace wkv
