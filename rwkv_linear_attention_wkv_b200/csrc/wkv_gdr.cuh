@@ -186,6 +186,26 @@ __device__ __forceinline__ int64_t sequence(const GdrArgs& a, int seq, int& len)
   return t0;
 }
 
+// The sequence that comes `rank`-th when the longest come first: a walk is as long as its sequence,
+// and a long one that starts last leaves the SMs idle (17 sequences of 9001 tokens, 32 x 128 heads:
+// XXX). Up to 64 packed sequences; more than that are taken as they come. Whole warps.
+__device__ __forceinline__ int by_length(const GdrArgs& a, int rank, int lane) {
+  if (a.offsets == nullptr || a.n_seqs > 64) return rank;
+  int len[2] = {-1, -1}, before[2] = {0, 0};
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+    if (p * 32 + lane < a.n_seqs) sequence(a, p * 32 + lane, len[p]);
+  for (int j = 0; j < a.n_seqs; ++j) {
+    const int other = __shfl_sync(0xffffffffu, j < 32 ? len[0] : len[1], j & 31);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      before[p] += other > len[p] || (other == len[p] && j < p * 32 + lane) ? 1 : 0;
+  }
+  const unsigned lo = __ballot_sync(0xffffffffu, lane < a.n_seqs && before[0] == rank);
+  const unsigned hi = __ballot_sync(0xffffffffu, lane + 32 < a.n_seqs && before[1] == rank);
+  return lo != 0 ? __ffs(lo) - 1 : 31 + __ffs(hi);
+}
+
 // A running log2-decay as an unevaluated sum of two floats (48 bits): decays between two tokens
 // are differences of such sums, and a strong decay earlier must not cost later ones their digits.
 // (fp64 took 4 times as long here: its unit is slow and its shuffles come in pairs.)

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
   constexpr int kSplitRows = N / X::kVRows;
   const int part = blockIdx.x % kSplitRows;
   const int sh = blockIdx.x / kSplitRows;
-  const int seq = sh / a.H, h = sh % a.H, hk = h / (a.H / a.Hk);
+  const int seq = by_length(a, sh / a.H, lane), h = sh % a.H, hk = h / (a.H / a.Hk);
   int len;
   const int64_t t0 = sequence(a, seq, len);
   const int steps = (len + X::kStep - 1) / X::kStep;
