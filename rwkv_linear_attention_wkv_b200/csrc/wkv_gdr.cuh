@@ -188,7 +188,7 @@ __device__ __forceinline__ int64_t sequence(const GdrArgs& a, int seq, int& len)
 
 // The sequence that comes `rank`-th when the longest come first: a walk is as long as its sequence,
 // and a long one that starts last leaves the SMs idle (17 sequences of 9001 tokens, 32 x 128 heads:
-// XXX). Up to 64 packed sequences; more than that are taken as they come. Whole warps.
+// 466 us, 368 longest first). Up to 64 packed sequences; more are taken as they come. Whole warps.
 __device__ __forceinline__ int by_length(const GdrArgs& a, int rank, int lane) {
   if (a.offsets == nullptr || a.n_seqs > 64) return rank;
   int len[2] = {-1, -1}, before[2] = {0, 0};

@@ -27,7 +27,14 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _need(t, name, dtype, shape, device):
+def _need(t, name, dtype, shape, index):
+    """Refuses t unless it is a contiguous tensor of this dtype and shape on CUDA device `index`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and \
+                t.is_contiguous() and index >= 0:
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -38,52 +45,49 @@ def _need(t, name, dtype, shape, device):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
-def _run(fn, device, stream, *args):
-    """Calls fn(*args, stream) with `device` current."""
-    index = device.index
+def _run(fn, index, stream, *args):
+    """Calls fn(*args, stream) with CUDA device `index` current."""
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
-        rc = getattr(lib, fn)(*args, raw)
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, raw)
     else:
         with torch.cuda.device(index):
-            rc = getattr(lib, fn)(*args, raw)
+            rc = fn(*args, raw)
     if rc != 0:
-        raise WkvError(fn, rc)
+        raise WkvError(fn.__name__, rc)
 
 
-def _problem(q, v, lead, scale, seq_offsets=None):
-    """Dtype, device and problem of a call from q (*lead, Hk, N) and v (*lead, H, N)."""
-    n = len(lead)
+def _problem(q, v, n, scale, seq_offsets=None):
+    """Problem and device of a call from q (n dimensions, Hk, N) and v (n dimensions, H, N)."""
     if not _dims(q, "q", n + 2) or not _dims(v, "v", n + 2):
         raise ValueError(f"q and v must have {n + 2} dimensions")
     if v.dtype not in _DTYPES:
         raise TypeError(f"v must be torch.float32 or torch.bfloat16, got {v.dtype}")
-    shape = v.shape
+    shape, index = v.shape, v.get_device()
     p = GdrProblem(shape[0], shape[1] if n == 2 else 1, q.shape[n], shape[n], shape[n + 1], 0, None,
                    _DTYPES[v.dtype], scale)
     if seq_offsets is not None:
         if not _dims(seq_offsets, "seq_offsets", 1) or seq_offsets.numel() < 1:
             raise ValueError("seq_offsets must hold one offset more than there are sequences")
-        _need(seq_offsets, "seq_offsets", torch.int32, seq_offsets.shape, v.device)
+        _need(seq_offsets, "seq_offsets", torch.int32, seq_offsets.shape, index)
         if shape[0] != 1:
             raise ValueError("with seq_offsets the sequences are packed into one row (B = 1)")
         p.n_seqs = seq_offsets.numel() - 1
         p.seq_offsets = seq_offsets.data_ptr()
-    return p
+    return p, index
 
 
-def _inputs(q, k, v, g, beta, lead):
-    dt, dev = v.dtype, v.device
-    qk, heads = q.shape, v.shape[:-1]
-    _need(v, "v", dt, v.shape, dev)
-    _need(q, "q", dt, lead + (qk[-2], v.shape[-1]), dev)
-    _need(k, "k", dt, qk, dev)
-    _need(g, "g", _F32, heads, dev)
-    _need(beta, "beta", _F32, heads, dev)
+def _inputs(q, k, v, g, beta, index):
+    dt, wide = v.dtype, v.shape
+    heads, qk = wide[:-1], q.shape
+    _need(v, "v", dt, wide, index)
+    _need(q, "q", dt, wide[:-2] + (qk[-2], wide[-1]), index)
+    _need(k, "k", dt, qk, index)
+    _need(g, "g", _F32, heads, index)
+    _need(beta, "beta", _F32, heads, index)
 
 
 def _sequences(p):
@@ -91,21 +95,22 @@ def _sequences(p):
 
 
 def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_state):
-    p = _problem(q, v, (0, 0), scale, seq_offsets)
-    _inputs(q, k, v, g, beta, v.shape[:2])
-    dev = v.device
+    p, index = _problem(q, v, 2, scale, seq_offsets)
+    _inputs(q, k, v, g, beta, index)
     if y is None:
         y = torch.empty_like(v)
     else:
-        _need(y, "y", v.dtype, v.shape, dev)
+        _need(y, "y", v.dtype, v.shape, index)
     states = (_sequences(p), p.H, p.N, p.N)
     if state is not None:
-        _need(state, "state", _F32, states, dev)
-    s1 = None
-    if want_state:
-        s1 = torch.empty(states, dtype=_F32, device=dev) if state_out is None else state_out
-        _need(s1, "state_out", _F32, states, dev)
-    return p, y, s1, dev
+        _need(state, "state", _F32, states, index)
+    if not want_state:
+        state_out = None
+    elif state_out is None:
+        state_out = torch.empty(states, dtype=_F32, device=v.device)
+    else:
+        _need(state_out, "state_out", _F32, states, index)
+    return p, y, state_out, index
 
 
 def wkv_gdr_forward(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None, y=None,
@@ -117,21 +122,22 @@ def wkv_gdr_forward(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None, y
     N, N) fp32 or None (zero). Returns (y, S_T), or (y, None) with want_state=False. state_out
     may be `state` itself.
     """
-    p, y, s1, dev = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_state)
-    _run("wkv_gdr_forward", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    p, y, s1, index = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out,
+                               want_state)
+    _run(lib.wkv_gdr_forward, index, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
          g.data_ptr(), beta.data_ptr(), y.data_ptr(), _at(state), _at(s1))
     return y, s1
 
 
-def _buffer(t, name, nbytes, device):
+def _buffer(t, name, nbytes, index):
     if t is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.device != device or not t.is_contiguous() or \
+    if t.get_device() != index or not t.is_contiguous() or \
             t.numel() * t.element_size() < nbytes:
         raise ValueError(f"{name} must be a contiguous CUDA tensor of at least {nbytes} bytes on "
-                         f"{device}")
+                         f"cuda:{index}")
     return t
 
 
@@ -140,10 +146,11 @@ def wkv_gdr_forward_checkpointed(q, k, v, g, beta, state=None, scale=1.0, seq_of
     """wkv_gdr_forward that also keeps what wkv_gdr_backward reads. Returns (y, S_T, workspace);
     hand the workspace (it is only read there) to the backward of the same inputs. seq_offsets
     must not decrease. state_out must not be `state` if `state` is needed again."""
-    p, y, s1, dev = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_state)
+    p, y, s1, index = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out,
+                               want_state)
     nbytes = int(lib.wkv_gdr_checkpoint_bytes(ctypes.byref(p)))
-    workspace = _buffer(workspace, "workspace", nbytes, dev)
-    _run("wkv_gdr_forward_checkpointed", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(),
+    workspace = _buffer(workspace, "workspace", nbytes, index)
+    _run(lib.wkv_gdr_forward_checkpointed, index, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(),
          v.data_ptr(), g.data_ptr(), beta.data_ptr(), y.data_ptr(), _at(state), _at(s1),
          _at(workspace), workspace.numel() * workspace.element_size())
     return y, s1, workspace
@@ -157,34 +164,35 @@ def wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=None, scale=1.0
 
     grads: such a dict to write into. Rows of the gradients that no packed sequence covers are
     left as they were (uninitialised without `grads`)."""
-    p = _problem(q, v, (0, 0), scale, seq_offsets)
-    _inputs(q, k, v, g, beta, v.shape[:2])
-    dev = v.device
-    _need(dy, "dy", v.dtype, v.shape, dev)
-    states = torch.Size((_sequences(p), p.H, p.N, p.N))
+    p, index = _problem(q, v, 2, scale, seq_offsets)
+    _inputs(q, k, v, g, beta, index)
+    _need(dy, "dy", v.dtype, v.shape, index)
+    states = (_sequences(p), p.H, p.N, p.N)
     if grad_state is not None:
-        _need(grad_state, "grad_state", _F32, states, dev)
-    shapes = {"dq": (q.dtype, q.shape), "dk": (q.dtype, q.shape), "dv": (v.dtype, v.shape),
-              "dg": (_F32, g.shape), "dbeta": (_F32, g.shape)}
-    if want_dstate:
-        shapes["dstate"] = (_F32, states)
+        _need(grad_state, "grad_state", _F32, states, index)
     if grads is None:
-        grads = {n: torch.empty(s, dtype=t, device=dev) for n, (t, s) in shapes.items()}
+        grads = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+                 "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
+        if want_dstate:
+            grads["dstate"] = torch.empty(states, dtype=_F32, device=v.device)
     else:
-        for n, (t, s) in shapes.items():
-            _need(grads.get(n), n, t, s, dev)
-    nbytes = int(lib.wkv_gdr_checkpoint_bytes(ctypes.byref(p)))
+        for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
+            _need(grads.get(n), n, t.dtype, t.shape, index)
+        if want_dstate:
+            _need(grads.get("dstate"), "dstate", _F32, states, index)
+    problem = ctypes.byref(p)
+    nbytes = int(lib.wkv_gdr_checkpoint_bytes(problem))
     if workspace is None:
         raise TypeError("workspace must be the forward's")
-    _buffer(workspace, "workspace", nbytes, dev)
-    scratch = _buffer(scratch, "scratch",
-                      int(lib.wkv_gdr_backward_workspace_bytes(ctypes.byref(p))), dev)
-    _run("wkv_gdr_backward", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-         g.data_ptr(), beta.data_ptr(), dy.data_ptr(), _at(workspace), workspace.numel() * workspace.element_size(),
-         _at(grad_state), *[grads[n].data_ptr() for n in ("dq", "dk", "dv", "dg", "dbeta")],
-         _at(grads["dstate"]) if want_dstate else None, _at(scratch),
+    _buffer(workspace, "workspace", nbytes, index)
+    scratch = _buffer(scratch, "scratch", int(lib.wkv_gdr_backward_workspace_bytes(problem)), index)
+    _run(lib.wkv_gdr_backward, index, stream, problem, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         g.data_ptr(), beta.data_ptr(), dy.data_ptr(), workspace.data_ptr(),
+         workspace.numel() * workspace.element_size(), _at(grad_state),
+         *[grads[n].data_ptr() for n in ("dq", "dk", "dv", "dg", "dbeta")],
+         grads["dstate"].data_ptr() if want_dstate else None, scratch.data_ptr(),
          scratch.numel() * scratch.element_size())
-    return {n: grads.get(n) if n in shapes else None
+    return {n: grads[n] if n != "dstate" or want_dstate else None
             for n in ("dq", "dk", "dv", "dg", "dbeta", "dstate")}
 
 
@@ -195,22 +203,21 @@ def wkv_gdr_decode_step(q, k, v, g, beta, state, slots=None, scale=1.0, y=None, 
     (no slot twice; outside [0, len(state)): padding, the row is skipped and its y stays as it
     was), None = row i has state i. Returns y (n, H, N).
     """
-    p = _problem(q, v, (0,), scale)
-    _inputs(q, k, v, g, beta, v.shape[:1])
-    dev = v.device
+    p, index = _problem(q, v, 1, scale)
+    _inputs(q, k, v, g, beta, index)
     if not _dims(state, "state", 4):
         raise ValueError("state must be (slots, H, N, N)")
-    n_slots = state.shape[0]
-    _need(state, "state", _F32, (n_slots, p.H, p.N, p.N), dev)
+    n_slots, N = state.shape[0], p.N
+    _need(state, "state", _F32, (n_slots, p.H, N, N), index)
     if slots is not None:
-        _need(slots, "slots", torch.int32, (p.B,), dev)
+        _need(slots, "slots", torch.int32, (p.B,), index)
     elif n_slots < p.B:
         raise ValueError(f"state must have at least {p.B} slots, got {n_slots}")
     if y is None:
         y = torch.empty_like(v)
     else:
-        _need(y, "y", v.dtype, v.shape, dev)
-    _run("wkv_gdr_decode_step", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(),
+        _need(y, "y", v.dtype, v.shape, index)
+    _run(lib.wkv_gdr_decode_step, index, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(),
          v.data_ptr(), g.data_ptr(), beta.data_ptr(), y.data_ptr(), state.data_ptr(), n_slots,
          _at(slots))
     return y

@@ -9,7 +9,7 @@ import ctypes
 import torch
 
 from . import lib
-from .gdr import _DTYPES, _F32, _at, _need, _run
+from .gdr import _DTYPES, _F32, _at, _buffer, _need, _run
 
 _ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
 
@@ -33,19 +33,20 @@ def _problem(h, weight, gate, x, scale, next_weight, group, act, eps):
         raise ValueError("act must be 'none' without a gate, and not with one")
     if scale is not None and x is None:
         raise ValueError("scale is the residual's: it needs x")
-    shape, dt, dev = h.shape, h.dtype, h.device
+    shape, dt, index = h.shape, h.dtype, h.get_device()
     C = shape[-1]
     group = C if group is None else group
     if C and (group <= 0 or C % group):
         raise ValueError(f"group must divide C = {C}, got {group}")
-    _need(h, "h", dt, shape, dev)
+    _need(h, "h", dt, shape, index)
     for n, t in (("gate", gate), ("x", x)):
         if t is not None:
-            _need(t, n, dt, shape, dev)
+            _need(t, n, dt, shape, index)
     for n, t in (("weight", weight), ("scale", scale), ("next_weight", next_weight)):
         if t is not None:
-            _need(t, n, _F32, shape[-1:], dev)
-    return NormGateProblem(h.numel() // C if C else 0, C, group, _DTYPES[dt], _ACTS[act], eps)
+            _need(t, n, _F32, (C,), index)
+    return (NormGateProblem(h.numel() // C if C else 0, C, group, _DTYPES[dt], _ACTS[act], eps),
+            index)
 
 
 def wkv_norm_gate_forward(h, weight=None, gate=None, x=None, scale=None, next_weight=None,
@@ -55,20 +56,20 @@ def wkv_norm_gate_forward(h, weight=None, gate=None, x=None, scale=None, next_we
     scale, next_weight: fp32 (C,). gate (with act="none"), weight, x, scale and next_weight may
     be left out. group: default C. Returns (out, y), y None without next_weight; `out` may be h
     or x itself."""
-    p = _problem(h, weight, gate, x, scale, next_weight, group, act, eps)
-    dt, dev = h.dtype, h.device
+    p, index = _problem(h, weight, gate, x, scale, next_weight, group, act, eps)
+    dt = h.dtype
     if out is None:
         out = torch.empty_like(h)
     else:
-        _need(out, "out", dt, h.shape, dev)
+        _need(out, "out", dt, h.shape, index)
     if next_weight is None:
         if y is not None:
             raise ValueError("y needs next_weight")
     elif y is None:
         y = torch.empty_like(h)
     else:
-        _need(y, "y", dt, h.shape, dev)
-    _run("wkv_norm_gate_forward", dev, stream, ctypes.byref(p), h.data_ptr(), _at(weight), _at(gate),
+        _need(y, "y", dt, h.shape, index)
+    _run(lib.wkv_norm_gate_forward, index, stream, ctypes.byref(p), h.data_ptr(), _at(weight), _at(gate),
          _at(x), _at(scale), _at(next_weight), out.data_ptr(), _at(y))
     return out, y
 
@@ -86,21 +87,16 @@ def wkv_norm_gate_backward(h, weight, dout, gate=None, x=None, scale=None, next_
         raise ValueError("dout or dy must be given")
     if dy is not None and next_weight is None:
         raise ValueError("dy needs next_weight")
-    p = _problem(h, weight, gate, x, scale, next_weight, group, act, eps)
-    dt, dev = h.dtype, h.device
+    p, index = _problem(h, weight, gate, x, scale, next_weight, group, act, eps)
+    dt = h.dtype
     for n, t in (("dout", dout), ("dy", dy)):
         if t is not None:
-            _need(t, n, dt, h.shape, dev)
+            _need(t, n, dt, h.shape, index)
     like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
     g = {"dh": torch.empty_like(h), "dweight": like(weight), "dgate": like(gate), "dx": like(x),
          "dscale": like(scale), "dnext_weight": None if dy is None else like(next_weight)}
-    nbytes = wkv_norm_gate_workspace_bytes(p.R, p.C)
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or workspace.device != dev or \
-            workspace.numel() * workspace.element_size() < nbytes:
-        raise ValueError(f"workspace must be a CUDA tensor of at least {nbytes} bytes on {dev}")
-    _run("wkv_norm_gate_backward", dev, stream, ctypes.byref(p), h.data_ptr(), _at(weight), _at(gate),
+    workspace = _buffer(workspace, "workspace", wkv_norm_gate_workspace_bytes(p.R, p.C), index)
+    _run(lib.wkv_norm_gate_backward, index, stream, ctypes.byref(p), h.data_ptr(), _at(weight), _at(gate),
          _at(x), _at(scale), _at(next_weight), _at(dout), _at(dy), g["dh"].data_ptr(),
          _at(g["dweight"]), _at(g["dgate"]), _at(g["dx"]), _at(g["dscale"]), _at(g["dnext_weight"]),
          workspace.data_ptr(), workspace.numel() * workspace.element_size())
