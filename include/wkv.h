@@ -347,7 +347,16 @@ typedef struct wkv_gdr_problem {
   const int32_t* seq_offsets; /* device, n_seqs + 1; NULL: the B rows are the sequences */
   int dtype;                  /* wkv_dtype of q, k, v, y and their gradients */
   float scale;
+  /* Scratch of the two forwards (device, 16-byte aligned), or NULL. Long sequences with few heads
+   * (at least 1024 tokens, and four times as many SMs as 64-row head parts) are walked in segments
+   * side by side when it has wkv_gdr_forward_workspace_bytes(p) bytes, and whole, several times
+   * slower, when it has not. The results differ by roundings. */
+  void* workspace;
+  size_t workspace_bytes;
 } wkv_gdr_problem;
+
+/* For the current device; 0 where no scratch is of use. */
+WKV_API size_t wkv_gdr_forward_workspace_bytes(const wkv_gdr_problem* p);
 
 /*
  * Forward. s0: the initial states (NULL = zero); s1: the final states (NULL = not wanted;
@@ -366,7 +375,8 @@ WKV_API int wkv_gdr_forward(const wkv_gdr_problem* p, const void* q, const void*
  * fp32 (B, T, H); ds0 as the states. ds1 NULL = zero; ds0 NULL = not wanted, and may be ds1. dq
  * and dk are summed over the value heads that share them; every sum has a fixed order. No
  * gradient may overlap an input or another. workspace: device, 16-byte aligned, scratch of
- * wkv_gdr_backward_workspace_bytes(p) bytes. Tokens that no sequence covers have their rows of
+ * wkv_gdr_backward_workspace_bytes(p) bytes (for the current device; at least as many as the
+ * checkpoints, the rest is for walking in segments). Tokens that no sequence covers have their rows of
  * the gradients left as they were. The two calls need seq_offsets that, clamped, do not decrease.
  * Too small a buffer: WKV_ERR_INVALID_ARG.
  */

@@ -58,6 +58,7 @@ _SIGS = {
     "wkv_testing_backward_timeout": ([ctypes.c_uint64, _P], ctypes.c_int),
     "wkv_testing_forward_plain": ([_I, _I, _I] + [_P] * 6 + [ctypes.c_int, _P], ctypes.c_int),
     "wkv_gdr_forward": ([_P] * 9 + [_P], ctypes.c_int),
+    "wkv_gdr_forward_workspace_bytes": ([_P], ctypes.c_size_t),
     "wkv_gdr_checkpoint_bytes": ([_P], ctypes.c_size_t),
     "wkv_gdr_backward_workspace_bytes": ([_P], ctypes.c_size_t),
     "wkv_gdr_forward_checkpointed": ([_P] * 10 + [ctypes.c_size_t, _P], ctypes.c_int),

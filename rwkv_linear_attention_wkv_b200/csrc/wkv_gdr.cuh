@@ -206,6 +206,67 @@ __device__ __forceinline__ int by_length(const GdrArgs& a, int rank, int lane) {
   return lo != 0 ? __ffs(lo) - 1 : 31 + __ffs(hi);
 }
 
+// What a CTA walks: a sequence, or segment `s` of its `count`.
+struct Span {
+  int seq, s, count, slot;
+  int64_t t_seq, t0;  // first token of the sequence, of the span
+  int len;
+};
+// The span of number `index` (by rank of length, or of segment); false where there is none. Whole
+// warps.
+__device__ __forceinline__ bool find_span(const GdrArgs& a, const GdrSegs& g, int index, int lane,
+                                          Span& sp) {
+  sp.s = 0;
+  sp.count = 1;
+  sp.slot = index;
+  if (g.tokens == 0) {
+    sp.seq = by_length(a, index, lane);
+    sp.t_seq = sp.t0 = sequence(a, sp.seq, sp.len);
+    return true;
+  }
+  auto count_of = [&](int len) { return len <= g.tokens ? 1 : (len - 1) / g.tokens + 1; };
+  if (a.offsets == nullptr) {
+    sp.count = count_of(a.T);
+    sp.seq = index / sp.count;
+    sp.s = index % sp.count;
+  } else {  // up to 64 sequences
+    int count[2] = {0, 0}, upto[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      int len = 0;
+      if (p * 32 + lane < a.n_seqs) {
+        sequence(a, p * 32 + lane, len);
+        count[p] = count_of(len);
+      }
+      upto[p] = count[p];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int below = __shfl_up_sync(0xffffffffu, upto[p], d);
+        if (lane >= d) upto[p] += below;
+      }
+    }
+    upto[1] += __shfl_sync(0xffffffffu, upto[0], 31);
+    int found = -1, first = 0;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const unsigned who = __ballot_sync(0xffffffffu, index >= upto[p] - count[p] && index < upto[p]);
+      if (who != 0) {
+        found = p * 32 + __ffs(who) - 1;
+        first = __shfl_sync(0xffffffffu, upto[p] - count[p], __ffs(who) - 1);
+        sp.count = __shfl_sync(0xffffffffu, count[p], __ffs(who) - 1);
+      }
+    }
+    if (found < 0) return false;
+    sp.seq = found;
+    sp.s = index - first;
+  }
+  int len;
+  sp.t_seq = sequence(a, sp.seq, len);
+  sp.t0 = sp.t_seq + int64_t(sp.s) * g.tokens;
+  sp.len = min(len - sp.s * g.tokens, g.tokens);
+  return true;
+}
+
 // A running log2-decay as an unevaluated sum of two floats (48 bits): decays between two tokens
 // are differences of such sums, and a strong decay earlier must not cost later ones their digits.
 // (fp64 took 4 times as long here: its unit is slow and its shuffles come in pairs.)
@@ -524,6 +585,49 @@ __device__ __forceinline__ void put_state(float* to, const float (&S)[N / 8][4],
   }
 }
 
+// Rows r0.. of the identity.
+template <int N>
+__device__ __forceinline__ void unit_state(float (&S)[N / 8][4], int r0, int lane) {
+  const int row = r0 + (lane >> 2), col = 2 * (lane & 3);
+#pragma unroll
+  for (int n = 0; n < N / 8; ++n)
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      S[n][x] = row + (x >> 1) * 8 == n * 8 + col + (x & 1) ? 1.f : 0.f;
+}
+
+// Where a span's walk starts and what a summary (see GdrSegs) is of: S_in of this warp's rows.
+// False: the CTA has nothing to walk. `first` and `last`: of the walk's spans.
+template <int N, bool SUMMARY>
+__device__ __forceinline__ bool start_state(float (&S)[N / 8][4], const GdrArgs& a,
+                                            const GdrSegs& g, const Span& sp, bool first, bool last,
+                                            bool unit, int back, const float* given, int h, int r0,
+                                            int lane) {
+  const int64_t at = (int64_t(sp.seq) * a.H + h) * N * N + int64_t(r0) * N;
+  const int64_t slot_at = (int64_t(sp.slot) * a.H + h) * N * N + int64_t(r0) * N;
+  const float* const start = given == nullptr ? nullptr : given + at;
+  if (!SUMMARY) {
+    get_state<N>(S,
+                 g.tokens == 0 ? start
+                 : first       ? g.unit + slot_at
+                               : g.leave + slot_at - int64_t(back) * a.H * N * N,
+                 lane);
+    return true;
+  }
+  if (unit && first) {
+    // kept where the last span's result cannot overwrite it
+    get_state<N>(S, start, lane);
+    put_state<N>(g.unit + slot_at, S, lane);
+    return false;
+  }
+  if (last) return false;
+  if (unit)
+    unit_state<N>(S, r0, lane);
+  else
+    get_state<N>(S, first ? start : nullptr, lane);
+  return true;
+}
+
 // Four consumers and steps of two groups everywhere (heads of 128 are two CTAs). bf16: two
 // producers, 168 registers and two CTAs an SM where there is work for them, or four producers and
 // one CTA, which is quicker alone (us, singles / pairs: 1 x 2048 x 8 x 64: 134 / 121, 1 x 2048 x 8
@@ -531,12 +635,12 @@ __device__ __forceinline__ void put_state(float* to, const float (&S)[N / 8][4],
 // 128: 582 / 618). fp32 splits q and k on the way, which takes four producers always (8 x 1024 x
 // 64 x 64: 496 / 388, 1 x 2048 x 8 x 64: 253 / 194).
 enum GdrWalkForm { kGdrWalkSingles, kGdrWalkPairs, kGdrWalkError };
-inline GdrWalkForm gdr_walk_form(const GdrArgs& a) {
+inline GdrWalkForm gdr_walk_form(const GdrArgs& a, int64_t spans) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return kGdrWalkError;
-  return int64_t(a.n_seqs) * a.H * (a.N / 64) <= sms ? kGdrWalkPairs : kGdrWalkSingles;
+  return spans * a.H * (a.N / 64) <= sms ? kGdrWalkPairs : kGdrWalkSingles;
 }
 
 // The producers' part of both kernels. Step s of a walk has the tokens from s kStep, counted from

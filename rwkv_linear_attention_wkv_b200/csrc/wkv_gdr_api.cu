@@ -1,5 +1,6 @@
 // C-ABI entry points of the gated delta rule: argument checks, plan selection, launches.
 // Declarations and their documentation: include/wkv.h.
+#include <algorithm>
 #include <cstdint>
 
 #include "wkv_internal.h"
@@ -18,7 +19,7 @@ int check_problem(const wkv_gdr_problem* p, bool* empty) {
   if (p->dtype != WKV_DTYPE_F32 && p->dtype != WKV_DTYPE_BF16) return WKV_ERR_INVALID_ARG;
   const bool packed = p->seq_offsets != nullptr;
   if (packed && (p->n_seqs < 0 || p->B != 1)) return WKV_ERR_INVALID_ARG;
-  if (!aligned(p->seq_offsets, 4)) return WKV_ERR_ALIGNMENT;
+  if (!aligned(p->seq_offsets, 4) || !aligned(p->workspace, 16)) return WKV_ERR_ALIGNMENT;
   const int64_t seqs = packed ? p->n_seqs : p->B;
   if (seqs == 0 || p->H == 0) {
     *empty = true;
@@ -67,6 +68,25 @@ size_t saved_bytes(const wkv_gdr_problem* p) {
   return (s.tokens + s.states) * sizeof(float);
 }
 
+// The plan of segments for a walk with `bytes` of scratch at hand: none where they do not fit.
+int segments_in(const GdrArgs& a, void* scratch, size_t bytes, GdrSegs* segs) {
+  const int64_t need = gdr_plan_segments(a, segs);
+  if (need < 0) return WKV_ERR_CUDA;
+  if (need == 0 || scratch == nullptr || size_t(need) > bytes) {
+    *segs = GdrSegs();
+    return WKV_OK;
+  }
+  segs->leave = static_cast<float*>(scratch);
+  segs->unit = segs->leave + size_t(segs->slots) * a.H * a.N * a.N;
+  return WKV_OK;
+}
+size_t segment_bytes(const wkv_gdr_problem* p) {
+  bool empty;
+  if (check_problem(p, &empty) != WKV_OK || empty || p->T == 0) return 0;
+  GdrSegs segs;
+  return size_t(std::max<int64_t>(0, gdr_plan_segments(args_of(p), &segs)));
+}
+
 // Forward, with somewhere to put the checkpoints or without.
 int forward(const wkv_gdr_problem* p, const void* q, const void* k, const void* v, const float* g,
             const float* beta, void* y, const float* s0, float* s1, bool keep, void* saved,
@@ -82,10 +102,12 @@ int forward(const wkv_gdr_problem* p, const void* q, const void* k, const void* 
   GdrArgs a = args_of(p);
   if (a.T == 0) return pass_state(s0, s1, size_t(a.n_seqs) * a.H * a.N * a.N * 4, stream);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.y = y; a.s0 = s0; a.s1 = s1;
-  if (!keep) return launch_gdr_chunked(a, nullptr, nullptr, stream);
-  if (saved == nullptr || saved_size < saved_bytes(p)) return WKV_ERR_INVALID_ARG;
-  float* e = static_cast<float*>(saved);
-  return launch_gdr_chunked(a, e, e + saved_of(a).tokens, stream);
+  if (keep && (saved == nullptr || saved_size < saved_bytes(p))) return WKV_ERR_INVALID_ARG;
+  float* const e = keep ? static_cast<float*>(saved) : nullptr;
+  float* const states = keep ? e + saved_of(a).tokens : nullptr;
+  GdrSegs segs;
+  if (int rc = segments_in(a, p->workspace, p->workspace_bytes, &segs)) return rc;
+  return launch_gdr_chunked(a, segs, e, states, stream);
 }
 
 }  // namespace
@@ -99,8 +121,11 @@ WKV_API int wkv_gdr_forward(const wkv_gdr_problem* p, const void* q, const void*
 }
 
 WKV_API size_t wkv_gdr_checkpoint_bytes(const wkv_gdr_problem* p) { return saved_bytes(p); }
+WKV_API size_t wkv_gdr_forward_workspace_bytes(const wkv_gdr_problem* p) {
+  return segment_bytes(p);
+}
 WKV_API size_t wkv_gdr_backward_workspace_bytes(const wkv_gdr_problem* p) {
-  return saved_bytes(p);
+  return saved_bytes(p) + segment_bytes(p);
 }
 
 WKV_API int wkv_gdr_forward_checkpointed(const wkv_gdr_problem* p, const void* q, const void* k,
@@ -143,7 +168,11 @@ WKV_API int wkv_gdr_backward(const wkv_gdr_problem* p, const void* q, const void
   b.du = static_cast<float*>(workspace);
   b.dstates = b.du + s.tokens;
   b.dq = dq; b.dk = dk; b.dv = dv; b.dg = dg; b.dbeta = dbeta; b.ds0 = ds0;
-  return launch_gdr_backward(b, stream);
+  GdrSegs segs;
+  const size_t used = saved_bytes(p);
+  if (int rc = segments_in(b.p, static_cast<char*>(workspace) + used, workspace_bytes - used, &segs))
+    return rc;
+  return launch_gdr_backward(b, segs, stream);
 }
 
 WKV_API int wkv_gdr_decode_step(const wkv_gdr_problem* p, const void* q, const void* k,

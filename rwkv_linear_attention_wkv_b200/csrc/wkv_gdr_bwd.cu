@@ -41,9 +41,10 @@ __device__ __forceinline__ void mma_exact_a(float (&c)[2][4], const uint32_t (&a
     for (int n = 0; n < 2; ++n) mma(c[n], a, b[p][2 * n], b[p][2 * n + 1]);
 }
 
-template <typename T, int N, int NC, int NG, int NP, int CTAS>
+// SUMMARY: as the forward's, of the gradient that enters a segment at its end.
+template <typename T, int N, int NC, int NG, int NP, int CTAS, bool SUMMARY>
 __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
-    gdr_chain_kernel(GdrBwdArgs b) {
+    gdr_chain_kernel(GdrBwdArgs b, GdrSegs segs) {
   using X = Shape<T, N, NC, NG, NP>;
   constexpr int P = X::kParts;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -51,12 +52,17 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t4 = lane & 3;
-  constexpr int kSplitRows = N / X::kVRows;
-  const int part = blockIdx.x % kSplitRows;
-  const int sh = blockIdx.x / kSplitRows;
-  const int seq = by_length(a, sh / a.H, lane), h = sh % a.H, hk = h / (a.H / a.Hk);
-  int len;
-  const int64_t t0 = sequence(a, seq, len);
+  constexpr int kSplitRows = N / X::kVRows, kParts = SUMMARY ? 2 * kSplitRows : kSplitRows;
+  const int part = blockIdx.x % kParts % kSplitRows;
+  const bool unit = SUMMARY && blockIdx.x % kParts >= kSplitRows;
+  const int sh = blockIdx.x / kParts;
+  const int h = sh % a.H, hk = h / (a.H / a.Hk);
+  Span sp;
+  if (!find_span(a, segs, sh / a.H, lane, sp)) return;
+  const int len = sp.len;
+  const int64_t t0 = sp.t0;
+  const bool first_span = sp.s == sp.count - 1, last_span = sp.s == 0;  // of the walk
+  if (SUMMARY && warp >= NC && (unit ? first_span || last_span : last_span)) return;
   const int steps = (len + X::kStep - 1) / X::kStep;
   GroupMats* const mats = reinterpret_cast<GroupMats*>(smem + X::kOffMats);  // [2][NG]
   const int64_t v_row = int64_t(a.H) * N;
@@ -72,16 +78,17 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
 
   // -------------------------------------------------------------------- consumers
   const int r0 = part * X::kVRows + warp * 16;  // this warp's value channels
-  const int64_t state_at = ((int64_t(seq) * a.H + h) * N + r0) * N;
   float S[N / 8][4];  // dD: 16 rows x N columns
-  get_state<N>(S, b.ds1 == nullptr ? nullptr : b.ds1 + state_at, lane);
+  if (!start_state<N, SUMMARY>(S, a, segs, sp, first_span, last_span, unit, -1, b.ds1, h, r0, lane))
+    return;
   T* dv = static_cast<T*>(b.dv) + t0 * v_row + int64_t(h) * N + r0;
   float* du = b.du + t0 * v_row + int64_t(h) * N + r0;
   __nv_bfloat16* const stage =
       reinterpret_cast<__nv_bfloat16*>(smem + X::kOffY) + warp * kG * kStagePitch;
   constexpr int kChunk = gdr_chunk(X::kBf16, N);
-  float* const dstates = b.dstates + gdr_chunk_base(a, seq, t0) * a.H * N * N +
-                         (int64_t(h) * N + r0) * N;
+  float* const dstates =
+      b.dstates + (gdr_chunk_base(a, sp.seq, sp.t_seq) + (t0 - sp.t_seq) / kChunk) * a.H * N * N +
+      (int64_t(h) * N + r0) * N;
 
   __syncthreads();  // the first step is prepared
   for (int i = 0; i < steps; ++i) {
@@ -89,7 +96,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
     for (int gi = NG - 1; gi >= 0; --gi) {
       const int first = first_of(i) + gi * kG;
       if (first >= len) continue;
-      if ((first + kG) % kChunk == 0 || first + kG >= len)
+      if (!SUMMARY && ((first + kG) % kChunk == 0 || first + kG >= len))
         put_state<N>(dstates + int64_t(first / kChunk) * a.H * N * N, S, lane);
       const GroupMats& m = mats[(i & 1) * NG + gi];
       const uint32_t grp = uint32_t(gi * kG * X::kPitch) * 2u;
@@ -100,16 +107,21 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
       const uint32_t to = at_tokens(lane, X::kPitch) + grp;
 #pragma unroll
       for (int c = 0; c < N; c += 16) {
-        uint32_t sp[3][4], kb[P][4];
+        uint32_t parts[3][4], kb[P][4];
 #pragma unroll
         for (int p = 0; p < P; ++p) ldsm4(kb[p], tile(i, 0, p) + to + c * 2);
-        split_tiles(S[c / 8], S[c / 8 + 1], sp);
-        mma_pairs<P, true>(xm, xc, sp, kb);
+        split_tiles(S[c / 8], S[c / 8 + 1], parts);
+        mma_pairs<P, true>(xm, xc, parts, kb);
       }
       // R^T
       float vv[2][4], r[2][4];
       uint32_t raw[4], ap[3][4], fb[3][4];
       get_tokens<T, X>(vv, raw, smem + X::kOffV + (i % 3) * X::kVTile, gi * kG, warp * 16, lane);
+      if (SUMMARY && unit) {
+        zero(vv[0]);
+        zero(vv[1]);
+        raw[0] = raw[1] = raw[2] = raw[3] = 0u;
+      }
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(fb[p]) = m.read[p][lane];
       zero(r[0]);
@@ -171,12 +183,17 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
 #pragma unroll
         for (int n = 0; n < 2; ++n) scale_add(S[c / 8 + n], end, d[n]);
       }
+      if (SUMMARY) continue;
       put_tokens<float>(du + first * v_row, v_row, r, len - first, nullptr, lane);
       put_tokens<T>(dv + first * v_row, v_row, de, len - first, stage, lane);
     }
     __syncthreads();
   }
-  if (b.ds0 != nullptr) put_state<N>(b.ds0 + state_at, S, lane);
+  if (SUMMARY)
+    put_state<N>((unit ? segs.unit : segs.leave) + (int64_t(sp.slot) * a.H + h) * N * N + r0 * N, S,
+                 lane);
+  else if (last_span && b.ds0 != nullptr)
+    put_state<N>(b.ds0 + (int64_t(sp.seq) * a.H + h) * N * N + r0 * N, S, lane);
 }
 
 // ---- the second kernel ----------------------------------------------------------------------
@@ -656,36 +673,55 @@ bool allow_smem(K* kernel, int bytes) {
          cudaSuccess;
 }
 
-template <typename T, int N, int NC, int NG, int NP, int CTAS>
-int launch(const GdrBwdArgs& b, cudaStream_t stream) {
-  using X = Shape<T, N, NC, NG, NP>;
-  using Y = Chunk<T, N>;
-  auto* chain = gdr_chain_kernel<T, N, NC, NG, NP, CTAS>;
-  auto* rest = gdr_chunk_kernel<T, N>;
-  if (!allow_smem(chain, X::kSmem) || !allow_smem(rest, Y::kSmem)) return WKV_ERR_CUDA;
-  const unsigned grid = unsigned(int64_t(b.p.n_seqs) * b.p.H * (N / X::kVRows));
-  chain<<<grid, X::kThreads, X::kSmem, stream>>>(b);
-  if (cudaPeekAtLastError() != cudaSuccess) return WKV_ERR_CUDA;
-  rest<<<unsigned(gdr_chunks(b.p) * b.p.Hk), Y::kThreads, Y::kSmem, stream>>>(b);
+template <bool SUMMARY, typename T, int N, int NP, int CTAS>
+int chain(const GdrBwdArgs& b, const GdrSegs& segs, cudaStream_t stream) {
+  using X = Shape<T, N, 4, 2, NP>;
+  auto* kernel = gdr_chain_kernel<T, N, 4, 2, NP, CTAS, SUMMARY>;
+  if (!allow_smem(kernel, X::kSmem)) return WKV_ERR_CUDA;
+  const int64_t spans = segs.tokens == 0 ? b.p.n_seqs : segs.slots;
+  kernel<<<unsigned(spans * b.p.H * (N / X::kVRows) * (SUMMARY ? 2 : 1)), X::kThreads, X::kSmem,
+           stream>>>(b, segs);
   return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+}
+
+template <typename T, int N>
+int rest(const GdrBwdArgs& b, cudaStream_t stream) {
+  using X = Chunk<T, N>;
+  auto* kernel = gdr_chunk_kernel<T, N>;
+  if (!allow_smem(kernel, X::kSmem)) return WKV_ERR_CUDA;
+  kernel<<<unsigned(gdr_chunks(b.p) * b.p.Hk), X::kThreads, X::kSmem, stream>>>(b);
+  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+}
+
+template <typename T, int N>
+int backward(const GdrBwdArgs& b, const GdrSegs& segs, cudaStream_t stream) {
+  constexpr bool kBf16 = sizeof(T) == 2;
+  const GdrWalkForm form = gdr_walk_form(b.p, segs.tokens == 0 ? b.p.n_seqs : segs.slots);
+  if (form == kGdrWalkError) return WKV_ERR_CUDA;
+  int rc = WKV_OK;
+  if (segs.tokens > 0) {
+    if constexpr (kBf16)
+      rc = chain<true, T, N, 2, 2>(b, segs, stream);
+    else
+      rc = chain<true, T, N, 4, 1>(b, segs, stream);
+    if (rc == WKV_OK) rc = launch_gdr_combine(b.p, segs, true, stream);
+  }
+  if (rc != WKV_OK) return rc;
+  if (!kBf16 || form == kGdrWalkPairs) {
+    rc = chain<false, T, N, 4, 1>(b, segs, stream);
+  } else {
+    if constexpr (kBf16) rc = chain<false, T, N, 2, 2>(b, segs, stream);
+  }
+  return rc == WKV_OK ? rest<T, N>(b, stream) : rc;
 }
 
 }  // namespace
 
-int launch_gdr_backward(const GdrBwdArgs& b, cudaStream_t stream) {
-  if (!b.p.bf16)
-    return b.p.N == 64 ? launch<float, 64, 4, 2, 4, 1>(b, stream)
-                     : launch<float, 128, 4, 2, 4, 1>(b, stream);
-  switch (gdr_walk_form(b.p)) {
-    case kGdrWalkPairs:
-      return b.p.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 4, 1>(b, stream)
-                       : launch<__nv_bfloat16, 128, 4, 2, 4, 1>(b, stream);
-    case kGdrWalkSingles:
-      return b.p.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 2, 2>(b, stream)
-                       : launch<__nv_bfloat16, 128, 4, 2, 2, 2>(b, stream);
-    default:
-      return WKV_ERR_CUDA;
-  }
+int launch_gdr_backward(const GdrBwdArgs& b, const GdrSegs& segs, cudaStream_t stream) {
+  if (b.p.bf16)
+    return b.p.N == 64 ? backward<__nv_bfloat16, 64>(b, segs, stream)
+                       : backward<__nv_bfloat16, 128>(b, segs, stream);
+  return b.p.N == 64 ? backward<float, 64>(b, segs, stream) : backward<float, 128>(b, segs, stream);
 }
 
 }  // namespace wkv

@@ -9,12 +9,8 @@
 // registers, and the products run transposed (channels x tokens): S_0 K^T and S_0 Q^T take the
 // state as operand a in place, e^T and the weighted e^T become operands as they come out.
 //
-// A CTA has one head of one sequence (or 64 of 128 rows of it): one producer warp per group of a
-// step of 16 or 32 tokens, and 4 or 8 consumer warps. While the consumers work on step i the
-// producers copy step i + 2 in (cp.async), and form A, its inverse and the masked read matrix of
-// step i + 1: everything that does not depend on the state. One barrier a step.
-#include <algorithm>
-
+// A CTA has 64 value channels of one head of one sequence (or of a segment of it): two or four
+// producer warps, see produce(), and four consumer warps.
 #include "wkv_gdr.cuh"
 
 namespace wkv {
@@ -23,21 +19,28 @@ using namespace gdr;
 
 namespace {
 
-template <typename T, int N, int NC, int NG, int NP, int CTAS>
+// SUMMARY: not the outputs but what a segment does to the state that enters it: the state leaving
+// it from zero (from s0 in a sequence's first segment), and from the identity without values.
+template <typename T, int N, int NC, int NG, int NP, int CTAS, bool SUMMARY>
 __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
-    gdr_fwd_kernel(GdrArgs a, float* e_out, float* checkpoints) {
+    gdr_fwd_kernel(GdrArgs a, GdrSegs segs, float* e_out, float* checkpoints) {
   using X = Shape<T, N, NC, NG, NP>;
   constexpr int P = X::kParts;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t4 = lane & 3;
-  constexpr int kSplitRows = N / X::kVRows;
-  const int part = blockIdx.x % kSplitRows;
-  const int sh = blockIdx.x / kSplitRows;
-  const int seq = by_length(a, sh / a.H, lane), h = sh % a.H, hk = h / (a.H / a.Hk);
-  int len;
-  const int64_t t0 = sequence(a, seq, len);
+  constexpr int kSplitRows = N / X::kVRows, kParts = SUMMARY ? 2 * kSplitRows : kSplitRows;
+  const int part = blockIdx.x % kParts % kSplitRows;
+  const bool unit = SUMMARY && blockIdx.x % kParts >= kSplitRows;
+  const int sh = blockIdx.x / kParts;
+  const int h = sh % a.H, hk = h / (a.H / a.Hk);
+  Span sp;
+  if (!find_span(a, segs, sh / a.H, lane, sp)) return;
+  const int len = sp.len;
+  const int64_t t0 = sp.t0;
+  const bool first_span = sp.s == 0, last_span = sp.s == sp.count - 1;
+  if (SUMMARY && warp >= NC && (unit ? first_span || last_span : last_span)) return;
   const int steps = (len + X::kStep - 1) / X::kStep;
   const GroupMats* const mats = reinterpret_cast<GroupMats*>(smem + X::kOffMats);  // [2][NG]
   const int64_t v_row = int64_t(a.H) * N;
@@ -51,13 +54,18 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
 
   // -------------------------------------------------------------------- consumers
   const int r0 = part * X::kVRows + warp * 16;  // this warp's value channels
-  const int64_t state_at = ((int64_t(seq) * a.H + h) * N + r0) * N;
   float S[N / 8][4];  // 16 rows x N columns: accumulator tiles of 8 columns
-  get_state<N>(S, a.s0 == nullptr ? nullptr : a.s0 + state_at, lane);
+  if (!start_state<N, SUMMARY>(S, a, segs, sp, first_span, last_span, unit, 1, a.s0, h, r0, lane))
+    return;
   T* y = static_cast<T*>(a.y) + t0 * v_row + int64_t(h) * N + r0;
   float* eo = e_out == nullptr ? nullptr : e_out + t0 * v_row + int64_t(h) * N + r0;
   __nv_bfloat16* const stage =
       reinterpret_cast<__nv_bfloat16*>(smem + X::kOffY) + warp * kG * kStagePitch;
+
+  constexpr int kChunk = gdr_chunk(X::kBf16, N);
+  if (checkpoints != nullptr)
+    checkpoints += ((gdr_chunk_base(a, sp.seq, sp.t_seq) + (t0 - sp.t_seq) / kChunk) * a.H + h) * N *
+                       N + r0 * N;
 
   __syncthreads();  // the first step is prepared
   for (int i = 0; i < steps; ++i) {
@@ -65,10 +73,8 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
     for (int gi = 0; gi < NG; ++gi) {
       const int first = i * X::kStep + gi * kG;
       if (first >= len) break;
-      if (checkpoints != nullptr && first % gdr_chunk(X::kBf16, N) == 0)
-        put_state<N>(checkpoints + ((gdr_chunk_base(a, seq, t0) + first / gdr_chunk(X::kBf16, N)) *
-                                        a.H + h) * N * N + r0 * N,
-                     S, lane);
+      if (!SUMMARY && checkpoints != nullptr && first % kChunk == 0)
+        put_state<N>(checkpoints + int64_t(first / kChunk) * a.H * N * N, S, lane);
       const GroupMats& m = mats[(i & 1) * NG + gi];
       const uint32_t grp = uint32_t(gi * kG * X::kPitch) * 2u;
       // S_0 K^T and S_0 Q^T
@@ -78,15 +84,15 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
       const uint32_t to = at_tokens(lane, X::kPitch) + grp;
 #pragma unroll
       for (int c = 0; c < N; c += 16) {
-        uint32_t sp[3][4], kb[P][4], qb[P][4];
+        uint32_t parts[3][4], kb[P][4], qb[P][4];
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           ldsm4(kb[p], tile(i, 0, p) + to + c * 2);
-          ldsm4(qb[p], tile(i, 1, p) + to + c * 2);
+          if (!SUMMARY) ldsm4(qb[p], tile(i, 1, p) + to + c * 2);
         }
-        split_tiles(S[c / 8], S[c / 8 + 1], sp);
-        mma_pairs<P, true>(xm, xc, sp, kb);
-        mma_pairs<P, !X::kBf16>(om, oc, sp, qb);
+        split_tiles(S[c / 8], S[c / 8 + 1], parts);
+        mma_pairs<P, true>(xm, xc, parts, kb);
+        if (!SUMMARY) mma_pairs<P, !X::kBf16>(om, oc, parts, qb);
       }
       // e: V^T - C_i X as accumulator, plus its product with (I + A)^-1 - I
       float e[2][4], ec[2][4];
@@ -94,6 +100,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
         float vv[2][4];
         uint32_t raw[4];
         get_tokens<T, X>(vv, raw, smem + X::kOffV + (i % 3) * X::kVTile, gi * kG, warp * 16, lane);
+        if (SUMMARY && unit) zero(vv[0]), zero(vv[1]);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const float2 d = *reinterpret_cast<const float2*>(m.decay + n * 8 + 2 * t4);
@@ -149,48 +156,70 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
 #pragma unroll
         for (int n = 0; n < 2; ++n) scale_add(S[c / 8 + n], end, d[n]);
       }
-      if (eo != nullptr) put_tokens<float>(eo + first * v_row, v_row, e, len - first, nullptr, lane);
-      put_tokens<T>(y + first * v_row, v_row, o, len - first, stage, lane);
+      if (!SUMMARY && eo != nullptr)
+        put_tokens<float>(eo + first * v_row, v_row, e, len - first, nullptr, lane);
+      if (!SUMMARY) put_tokens<T>(y + first * v_row, v_row, o, len - first, stage, lane);
     }
     __syncthreads();
   }
-  if (checkpoints != nullptr && len > 0) {
-    constexpr int kChunk = gdr_chunk(X::kBf16, N);
-    put_state<N>(checkpoints + ((gdr_chunk_base(a, seq, t0) + (len + kChunk - 1) / kChunk) * a.H +
-                                h) * N * N + r0 * N,
-                 S, lane);
+  if (SUMMARY) {
+    put_state<N>((unit ? segs.unit : segs.leave) + (int64_t(sp.slot) * a.H + h) * N * N + r0 * N, S,
+                 lane);
+    return;
   }
-  if (a.s1 != nullptr) put_state<N>(a.s1 + state_at, S, lane);
+  if (!last_span) return;
+  if (checkpoints != nullptr && len > 0)
+    put_state<N>(checkpoints + int64_t((len + kChunk - 1) / kChunk) * a.H * N * N, S, lane);
+  if (a.s1 != nullptr)
+    put_state<N>(a.s1 + (int64_t(sp.seq) * a.H + h) * N * N + r0 * N, S, lane);
 }
 
-template <typename T, int N, int NC, int NG, int NP, int CTAS>
-int launch(const GdrArgs& a, float* e, float* checkpoints, cudaStream_t stream) {
+template <bool SUMMARY, typename T, int N, int NC, int NG, int NP, int CTAS>
+int launch(const GdrArgs& a, const GdrSegs& segs, float* e, float* checkpoints,
+           cudaStream_t stream) {
   using X = Shape<T, N, NC, NG, NP>;
-  auto* kernel = gdr_fwd_kernel<T, N, NC, NG, NP, CTAS>;
+  auto* kernel = gdr_fwd_kernel<T, N, NC, NG, NP, CTAS, SUMMARY>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, X::kSmem) !=
       cudaSuccess)
     return WKV_ERR_CUDA;
-  const unsigned grid = unsigned(int64_t(a.n_seqs) * a.H * (N / X::kVRows));
-  kernel<<<grid, X::kThreads, X::kSmem, stream>>>(a, e, checkpoints);
+  const int64_t spans = segs.tokens == 0 ? a.n_seqs : segs.slots;
+  kernel<<<unsigned(spans * a.H * (N / X::kVRows) * (SUMMARY ? 2 : 1)), X::kThreads, X::kSmem,
+           stream>>>(a, segs, e, checkpoints);
   return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+}
+
+template <typename T, int N, int NP, int CTAS>
+int walk(const GdrArgs& a, const GdrSegs& segs, float* e, float* checkpoints, cudaStream_t stream) {
+  return launch<false, T, N, 4, 2, NP, CTAS>(a, segs, e, checkpoints, stream);
+}
+template <typename T, int N, int NP, int CTAS>
+int summary(const GdrArgs& a, const GdrSegs& segs, cudaStream_t stream) {
+  return launch<true, T, N, 4, 2, NP, CTAS>(a, segs, nullptr, nullptr, stream);
 }
 
 }  // namespace
 
-int launch_gdr_chunked(const GdrArgs& a, float* e, float* checkpoints, cudaStream_t stream) {
-  if (!a.bf16)
-    return a.N == 64 ? launch<float, 64, 4, 2, 4, 1>(a, e, checkpoints, stream)
-                     : launch<float, 128, 4, 2, 4, 1>(a, e, checkpoints, stream);
-  switch (gdr_walk_form(a)) {
-    case kGdrWalkPairs:
-      return a.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 4, 1>(a, e, checkpoints, stream)
-                       : launch<__nv_bfloat16, 128, 4, 2, 4, 1>(a, e, checkpoints, stream);
-    case kGdrWalkSingles:
-      return a.N == 64 ? launch<__nv_bfloat16, 64, 4, 2, 2, 2>(a, e, checkpoints, stream)
-                       : launch<__nv_bfloat16, 128, 4, 2, 2, 2>(a, e, checkpoints, stream);
-    default:
-      return WKV_ERR_CUDA;
+int launch_gdr_chunked(const GdrArgs& a, const GdrSegs& segs, float* e, float* checkpoints,
+                       cudaStream_t stream) {
+  using bf16 = __nv_bfloat16;
+  const GdrWalkForm form = gdr_walk_form(a, segs.tokens == 0 ? a.n_seqs : segs.slots);
+  if (form == kGdrWalkError) return WKV_ERR_CUDA;
+  if (segs.tokens > 0) {
+    int rc = a.bf16 ? (a.N == 64 ? summary<bf16, 64, 2, 2>(a, segs, stream)
+                                 : summary<bf16, 128, 2, 2>(a, segs, stream))
+                    : (a.N == 64 ? summary<float, 64, 4, 1>(a, segs, stream)
+                                 : summary<float, 128, 4, 1>(a, segs, stream));
+    if (rc == WKV_OK) rc = launch_gdr_combine(a, segs, false, stream);
+    if (rc != WKV_OK) return rc;
   }
+  if (!a.bf16)
+    return a.N == 64 ? walk<float, 64, 4, 1>(a, segs, e, checkpoints, stream)
+                     : walk<float, 128, 4, 1>(a, segs, e, checkpoints, stream);
+  if (form == kGdrWalkPairs)
+    return a.N == 64 ? walk<bf16, 64, 4, 1>(a, segs, e, checkpoints, stream)
+                     : walk<bf16, 128, 4, 1>(a, segs, e, checkpoints, stream);
+  return a.N == 64 ? walk<bf16, 64, 2, 2>(a, segs, e, checkpoints, stream)
+                   : walk<bf16, 128, 2, 2>(a, segs, e, checkpoints, stream);
 }
 
 }  // namespace wkv

@@ -163,10 +163,23 @@ struct GdrArgs {
 };
 // Token by token, the state in registers.
 int launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream);
+// Walks in segments, side by side, where a few heads would leave most SMs idle (wkv_gdr_seg.cu).
+// A state leaves a segment as S M + B, M and B from the segment's tokens alone.
+struct GdrSegs {
+  int tokens = 0;  // of a segment (a multiple of every chunk's); 0: sequences are walked whole
+  int slots = 0;   // segments, numbered through the sequences (packed: as many as there may be)
+  float* leave = nullptr;  // (slots, H, N, N): B, then the state leaving a segment
+  float* unit = nullptr;   // (slots, H, N, N): M; for a walk's first segment the state it starts from
+};
+// The plan for a problem; reverse or not, the same. < 0 on a CUDA error, else the scratch in bytes.
+int64_t gdr_plan_segments(const GdrArgs& a, GdrSegs* segs);
+// leave[s] for the inner segments of every walk, from the walk's first to its last but one.
+int launch_gdr_combine(const GdrArgs& a, const GdrSegs& segs, bool reverse, cudaStream_t stream);
 // In groups of 16 tokens on the matrix units. e (tokens, H, N) and checkpoints (chunks, H, N, N)
 // are what the backward reads: every token's error before its write, and the state entering
 // every chunk of gdr_chunk() tokens of every sequence, and leaving the last; null = not wanted.
-int launch_gdr_chunked(const GdrArgs& a, float* e, float* checkpoints, cudaStream_t stream);
+int launch_gdr_chunked(const GdrArgs& a, const GdrSegs& segs, float* e, float* checkpoints,
+                       cudaStream_t stream);
 // Tokens of a chunk: 32 where the chunk's operands would not fit shared memory at 64.
 __host__ __device__ constexpr int gdr_chunk(bool bf16, int N) { return !bf16 && N == 128 ? 32 : 64; }
 // Number of a sequence's first chunk. After a sequence's chunks comes one that holds the state
@@ -199,7 +212,7 @@ struct GdrBwdArgs {
   float* dbeta;
   float* ds0;
 };
-int launch_gdr_backward(const GdrBwdArgs& a, cudaStream_t stream);
+int launch_gdr_backward(const GdrBwdArgs& a, const GdrSegs& segs, cudaStream_t stream);
 
 // Norm, gate, residual and next norm around a block (wkv_norm_gate.cu); null pointers are what
 // the entry points let a caller leave out.

@@ -20,7 +20,12 @@ class GdrProblem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hk", ctypes.c_int64),
                 ("H", ctypes.c_int64), ("N", ctypes.c_int64), ("n_seqs", ctypes.c_int64),
                 ("seq_offsets", ctypes.c_void_p), ("dtype", ctypes.c_int),
-                ("scale", ctypes.c_float)]
+                ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+# Fewer tokens than this are never walked in segments (include/wkv.h).
+_SEGMENTED = 1024
 
 
 def _at(t):
@@ -60,6 +65,23 @@ def _run(fn, index, stream, *args):
         raise WkvError(fn.__name__, rc)
 
 
+def _scratch(nbytes, index, stream):
+    """Uninitialised bytes for one call: on another stream than the current one they stay taken
+    until that stream has passed the call."""
+    t = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _bytes(fn, problem, index):
+    """A size that depends on the device."""
+    if index == torch._C._cuda_getDevice():
+        return int(fn(problem))
+    with torch.cuda.device(index):
+        return int(fn(problem))
+
+
 def _problem(q, v, n, scale, seq_offsets=None):
     """Problem and device of a call from q (n dimensions, Hk, N) and v (n dimensions, H, N)."""
     if not _dims(q, "q", n + 2) or not _dims(v, "v", n + 2):
@@ -68,7 +90,7 @@ def _problem(q, v, n, scale, seq_offsets=None):
         raise TypeError(f"v must be torch.float32 or torch.bfloat16, got {v.dtype}")
     shape, index = v.shape, v.get_device()
     p = GdrProblem(shape[0], shape[1] if n == 2 else 1, q.shape[n], shape[n], shape[n + 1], 0, None,
-                   _DTYPES[v.dtype], scale)
+                   _DTYPES[v.dtype], scale, None, 0)
     if seq_offsets is not None:
         if not _dims(seq_offsets, "seq_offsets", 1) or seq_offsets.numel() < 1:
             raise ValueError("seq_offsets must hold one offset more than there are sequences")
@@ -94,7 +116,8 @@ def _sequences(p):
     return p.n_seqs if p.seq_offsets else p.B
 
 
-def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_state):
+def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_state, stream):
+    """Problem, outputs, device and scratch (to be held until the call is made) of a forward."""
     p, index = _problem(q, v, 2, scale, seq_offsets)
     _inputs(q, k, v, g, beta, index)
     if y is None:
@@ -110,7 +133,13 @@ def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_sta
         state_out = torch.empty(states, dtype=_F32, device=v.device)
     else:
         _need(state_out, "state_out", _F32, states, index)
-    return p, y, state_out, index
+    scratch = None
+    if p.T >= _SEGMENTED:
+        nbytes = _bytes(lib.wkv_gdr_forward_workspace_bytes, ctypes.byref(p), index)
+        if nbytes:
+            scratch = _scratch(nbytes, index, stream)
+            p.workspace, p.workspace_bytes = scratch.data_ptr(), nbytes
+    return p, y, state_out, index, scratch
 
 
 def wkv_gdr_forward(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None, y=None,
@@ -122,16 +151,16 @@ def wkv_gdr_forward(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None, y
     N, N) fp32 or None (zero). Returns (y, S_T), or (y, None) with want_state=False. state_out
     may be `state` itself.
     """
-    p, y, s1, index = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out,
-                               want_state)
+    p, y, s1, index, _held = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out,
+                                      want_state, stream)
     _run(lib.wkv_gdr_forward, index, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
          g.data_ptr(), beta.data_ptr(), y.data_ptr(), _at(state), _at(s1))
     return y, s1
 
 
-def _buffer(t, name, nbytes, index):
+def _buffer(t, name, nbytes, index, stream):
     if t is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+        return _scratch(nbytes, index, stream)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != index or not t.is_contiguous() or \
@@ -146,10 +175,10 @@ def wkv_gdr_forward_checkpointed(q, k, v, g, beta, state=None, scale=1.0, seq_of
     """wkv_gdr_forward that also keeps what wkv_gdr_backward reads. Returns (y, S_T, workspace);
     hand the workspace (it is only read there) to the backward of the same inputs. seq_offsets
     must not decrease. state_out must not be `state` if `state` is needed again."""
-    p, y, s1, index = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out,
-                               want_state)
+    p, y, s1, index, _held = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out,
+                                      want_state, stream)
     nbytes = int(lib.wkv_gdr_checkpoint_bytes(ctypes.byref(p)))
-    workspace = _buffer(workspace, "workspace", nbytes, index)
+    workspace = _buffer(workspace, "workspace", nbytes, index, stream)
     _run(lib.wkv_gdr_forward_checkpointed, index, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(),
          v.data_ptr(), g.data_ptr(), beta.data_ptr(), y.data_ptr(), _at(state), _at(s1),
          _at(workspace), workspace.numel() * workspace.element_size())
@@ -184,8 +213,10 @@ def wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=None, scale=1.0
     nbytes = int(lib.wkv_gdr_checkpoint_bytes(problem))
     if workspace is None:
         raise TypeError("workspace must be the forward's")
-    _buffer(workspace, "workspace", nbytes, index)
-    scratch = _buffer(scratch, "scratch", int(lib.wkv_gdr_backward_workspace_bytes(problem)), index)
+    _buffer(workspace, "workspace", nbytes, index, stream)
+    if scratch is None:
+        nbytes = _bytes(lib.wkv_gdr_backward_workspace_bytes, problem, index)
+    scratch = _buffer(scratch, "scratch", nbytes, index, stream)
     _run(lib.wkv_gdr_backward, index, stream, problem, q.data_ptr(), k.data_ptr(), v.data_ptr(),
          g.data_ptr(), beta.data_ptr(), dy.data_ptr(), workspace.data_ptr(),
          workspace.numel() * workspace.element_size(), _at(grad_state),

@@ -95,7 +95,8 @@ def wkv_norm_gate_backward(h, weight, dout, gate=None, x=None, scale=None, next_
     like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
     g = {"dh": torch.empty_like(h), "dweight": like(weight), "dgate": like(gate), "dx": like(x),
          "dscale": like(scale), "dnext_weight": None if dy is None else like(next_weight)}
-    workspace = _buffer(workspace, "workspace", wkv_norm_gate_workspace_bytes(p.R, p.C), index)
+    workspace = _buffer(workspace, "workspace", wkv_norm_gate_workspace_bytes(p.R, p.C), index,
+                        stream)
     _run(lib.wkv_norm_gate_backward, index, stream, ctypes.byref(p), h.data_ptr(), _at(weight), _at(gate),
          _at(x), _at(scale), _at(next_weight), _at(dout), _at(dy), g["dh"].data_ptr(),
          _at(g["dweight"]), _at(g["dgate"]), _at(g["dx"]), _at(g["dscale"]), _at(g["dnext_weight"]),

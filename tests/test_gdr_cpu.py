@@ -61,7 +61,8 @@ def test_reference_gradients_are_differences(name):
 
 def problem(W, **over):
     from rwkv_linear_attention_wkv_b200.gdr import GdrProblem
-    x = dict(B=2, T=5, Hk=2, H=4, N=64, n_seqs=0, seq_offsets=None, dtype=1, scale=1.0)
+    x = dict(B=2, T=5, Hk=2, H=4, N=64, n_seqs=0, seq_offsets=None, dtype=1, scale=1.0,
+             workspace=None, workspace_bytes=0)
     x.update(over)
     return ctypes.byref(GdrProblem(*[x[n] for n, _ in GdrProblem._fields_]))
 
@@ -79,6 +80,8 @@ def test_forward_refusals(W):
                  dict(H=1 << 20, Hk=1), dict(seq_offsets=ok, B=1, n_seqs=1 << 30)):
         assert call(over) == 5, over
     assert call(dict(seq_offsets=ok + 2, B=1, n_seqs=2)) == 2
+    assert call(dict(workspace=ok + 8)) == 2
+    assert W.lib.wkv_gdr_forward_workspace_bytes(problem(W, T=100, H=1, Hk=1)) == 0
     for i in range(6):
         assert call(**{"p%d" % i: None}) == 1, i
     for i in (0, 1, 2, 5, 6, 7):

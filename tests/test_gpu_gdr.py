@@ -123,6 +123,43 @@ def test_forward_split_with_state_in_place(W, N):
     ref.assert_close(S, Sr, "state", head_dim=1)
 
 
+# long sequences of few heads are walked in segments of at least 256 tokens, side by side
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("N,B,T,Hk,H", [(64, 1, 1025, 1, 1), (64, 2, 1217, 1, 3), (128, 1, 1100, 1, 2),
+                                        (128, 3, 1024, 1, 1)])
+def test_forward_in_segments(W, N, B, T, Hk, H, dtype):
+    check(W, (B, T), Hk, H, N, dtype, state=T % 2 == 1, seed=T + N)
+
+
+@pytest.mark.parametrize("N", [64, 128])
+def test_forward_in_segments_strong_decays_and_state_in_place(W, N):
+    x = ref.inputs((1, 1100), 1, 1, N, FP32, 23, strong=True)
+    S = states(1, 1, N, 24)
+    yr, Sr = ref.rows(*x, 1.0, S)
+    S = S.cuda()
+    y, S1 = W.wkv_gdr_forward(*cuda(*x), state=S, state_out=S)
+    assert S1 is S
+    ref.assert_close(y, yr, "y", head_dim=2)
+    ref.assert_close(S, Sr, "state", head_dim=1)
+
+
+@pytest.mark.parametrize("N", [64, 128])
+def test_forward_packed_in_segments(W, N):
+    # one sequence of several segments, one of exactly two, one of one, an empty one
+    off = [3, 3, 1000, 1512, 1600]
+    T, H = 1700, 2
+    x = ref.inputs((1, T), 1, H, N, BF16, 25)
+    S0 = states(4, H, N, 26)
+    y = torch.full((1, T, H, N), 7.0, dtype=BF16, device="cuda")
+    _, S = W.wkv_gdr_forward(*cuda(*x), state=S0.cuda(), scale=0.5, y=y,
+                             seq_offsets=torch.tensor(off, dtype=torch.int32, device="cuda"))
+    yr, Sr = ref.rows(*x, 0.5, S0, list(zip(off[:-1], off[1:])))
+    assert bool((y[:, :3] == 7).all()) and bool((y[:, 1600:] == 7).all())
+    ref.assert_close(y[:, 3:1600], yr[:, 3:1600], "y", head_dim=2)
+    ref.assert_close(S, Sr, "state", head_dim=1)
+    assert torch.equal(S[0].cpu(), S0[0])
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("N", [64, 128])
 def test_decode_with_slots(W, N, dtype):

@@ -128,6 +128,26 @@ def test_backward_packed(W, N, dtype):
         assert bool((out[m][:, :2] == 7).all()) and bool((out[m][:, 166:] == 7).all())
 
 
+# long sequences of few heads: both walks in segments of at least 256 tokens, side by side
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("N,B,T,Hk,H", [(64, 1, 1025, 1, 2), (128, 1, 1100, 1, 1)])
+def test_backward_in_segments(W, N, B, T, Hk, H, dtype):
+    check(W, B, T, Hk, H, N, dtype, state=T % 2 == 1, seed=T + N)
+
+
+@pytest.mark.parametrize("N", [64, 128])
+def test_backward_packed_in_segments(W, N):
+    off = [3, 3, 1000, 1512, 1600]
+    T, H, n = 1700, 1, 4
+    x = ref.inputs((1, T), 1, H, N, FP32, 27)
+    dy = normal((1, T, H, N), 28)
+    S0, dS = 0.3 * normal((n, H, N, N), 29), 0.3 * normal((n, H, N, N), 30)
+    got = run(W, x, 0.5, dy, S0, dS, off)
+    want = gradients(x, 0.5, dy, S0, dS, [(0, a, b) for a, b in zip(off[:-1], off[1:])])
+    compare(got, want, FP32, slice(3, 1600))
+    assert torch.equal(got["dstate"][0].cpu(), dS[0])
+
+
 def test_backward_many_heads_and_repeats(W):
     # more chunks than the GPU holds at once; a second call gives the same bits (fixed orders),
     # and the workspace is only read
