@@ -9,7 +9,7 @@ import ctypes
 
 import torch
 
-from . import WkvError, _dims, lib
+from . import WkvError, lib
 
 _F32 = torch.float32
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -82,17 +82,25 @@ def _bytes(fn, problem, index):
         return int(fn(problem))
 
 
+def _shape(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t.shape
+
+
 def _problem(q, v, n, scale, seq_offsets=None):
     """Problem and device of a call from q (n dimensions, Hk, N) and v (n dimensions, H, N)."""
-    if not _dims(q, "q", n + 2) or not _dims(v, "v", n + 2):
+    heads, shape = _shape(q, "q"), _shape(v, "v")
+    if len(heads) != n + 2 or len(shape) != n + 2:
         raise ValueError(f"q and v must have {n + 2} dimensions")
-    if v.dtype not in _DTYPES:
+    dtype = _DTYPES.get(v.dtype)
+    if dtype is None:
         raise TypeError(f"v must be torch.float32 or torch.bfloat16, got {v.dtype}")
-    shape, index = v.shape, v.get_device()
-    p = GdrProblem(shape[0], shape[1] if n == 2 else 1, q.shape[n], shape[n], shape[n + 1], 0, None,
-                   _DTYPES[v.dtype], scale, None, 0)
+    p = GdrProblem(shape[0], shape[1] if n == 2 else 1, heads[n], shape[n], shape[n + 1], 0, None,
+                   dtype, scale, None, 0)
+    index = v.get_device()
     if seq_offsets is not None:
-        if not _dims(seq_offsets, "seq_offsets", 1) or seq_offsets.numel() < 1:
+        if len(_shape(seq_offsets, "seq_offsets")) != 1 or seq_offsets.numel() < 1:
             raise ValueError("seq_offsets must hold one offset more than there are sequences")
         _need(seq_offsets, "seq_offsets", torch.int32, seq_offsets.shape, index)
         if shape[0] != 1:
@@ -112,10 +120,6 @@ def _inputs(q, k, v, g, beta, index):
     _need(beta, "beta", _F32, heads, index)
 
 
-def _sequences(p):
-    return p.n_seqs if p.seq_offsets else p.B
-
-
 def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_state, stream):
     """Problem, outputs, device and scratch (to be held until the call is made) of a forward."""
     p, index = _problem(q, v, 2, scale, seq_offsets)
@@ -124,17 +128,18 @@ def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_sta
         y = torch.empty_like(v)
     else:
         _need(y, "y", v.dtype, v.shape, index)
-    states = (_sequences(p), p.H, p.N, p.N)
+    B, T, H, N = v.shape
+    states = (B if seq_offsets is None else p.n_seqs, H, N, N)
     if state is not None:
         _need(state, "state", _F32, states, index)
     if not want_state:
         state_out = None
     elif state_out is None:
-        state_out = torch.empty(states, dtype=_F32, device=v.device)
+        state_out = v.new_empty(states, dtype=_F32)
     else:
         _need(state_out, "state_out", _F32, states, index)
     scratch = None
-    if p.T >= _SEGMENTED:
+    if T >= _SEGMENTED:
         nbytes = _bytes(lib.wkv_gdr_forward_workspace_bytes, ctypes.byref(p), index)
         if nbytes:
             scratch = _scratch(nbytes, index, stream)
@@ -196,14 +201,15 @@ def wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=None, scale=1.0
     p, index = _problem(q, v, 2, scale, seq_offsets)
     _inputs(q, k, v, g, beta, index)
     _need(dy, "dy", v.dtype, v.shape, index)
-    states = (_sequences(p), p.H, p.N, p.N)
+    B, T, H, N = v.shape
+    states = (B if seq_offsets is None else p.n_seqs, H, N, N)
     if grad_state is not None:
         _need(grad_state, "grad_state", _F32, states, index)
     if grads is None:
         grads = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
                  "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
         if want_dstate:
-            grads["dstate"] = torch.empty(states, dtype=_F32, device=v.device)
+            grads["dstate"] = v.new_empty(states, dtype=_F32)
     else:
         for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
             _need(grads.get(n), n, t.dtype, t.shape, index)
@@ -236,14 +242,16 @@ def wkv_gdr_decode_step(q, k, v, g, beta, state, slots=None, scale=1.0, y=None, 
     """
     p, index = _problem(q, v, 1, scale)
     _inputs(q, k, v, g, beta, index)
-    if not _dims(state, "state", 4):
+    n, H, N = v.shape
+    pool = _shape(state, "state")
+    if len(pool) != 4:
         raise ValueError("state must be (slots, H, N, N)")
-    n_slots, N = state.shape[0], p.N
-    _need(state, "state", _F32, (n_slots, p.H, N, N), index)
+    n_slots = pool[0]
+    _need(state, "state", _F32, (n_slots, H, N, N), index)
     if slots is not None:
-        _need(slots, "slots", torch.int32, (p.B,), index)
-    elif n_slots < p.B:
-        raise ValueError(f"state must have at least {p.B} slots, got {n_slots}")
+        _need(slots, "slots", torch.int32, (n,), index)
+    elif n_slots < n:
+        raise ValueError(f"state must have at least {n} slots, got {n_slots}")
     if y is None:
         y = torch.empty_like(v)
     else:
