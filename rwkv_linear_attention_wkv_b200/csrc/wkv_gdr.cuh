@@ -15,9 +15,9 @@
 //
 // Precision: a state, and what is derived from it, is fp32; as an operand it is split into three
 // bf16 parts (24 bits), so that products with bf16 inputs (one part) take 3 instructions and
-// products of two split values 6 (hi hi, hi mid, mid hi, hi lo, lo hi, mid mid). fp32 inputs are
-// split into three parts as well. What only bf16 outputs see leaves out the third part (2^-17 of
-// a value against their own rounding of 2^-9).
+// products of two split values 6 (hi hi, hi mid, mid hi, hi lo, lo hi, mid mid: what is left out is
+// below 2^-22). fp32 inputs are split into three parts as well. What only bf16 outputs see leaves
+// out the third part (below 2^-15 of a value against their own rounding of 2^-9).
 #pragma once
 
 #include <cstdint>
@@ -71,14 +71,22 @@ __device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Two values as three packed bf16 parts.
+// Two values as three packed bf16 parts that add up to them: hi to the nearest, mid and lo by
+// cutting off (8 bits each). With integer adds, masks and byte permutes: packed conversions and
+// fp32x2 arithmetic take as many instructions, but wait for one another and for the matrix
+// instructions (16 such splits beside 16 matrix instructions, cycles a scheduler: 435 with
+// conversions, 298 this way; 129 for the matrix instructions alone).
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& mid,
                                        uint32_t& lo) {
-  __nv_bfloat162 h, m, l;
-  bf16_split3x2(make_float2(x, y), h, m, l);
-  hi = bits(h);
-  mid = bits(m);
-  lo = bits(l);
+  constexpr uint32_t kTop = 0xffff0000u;
+  const uint32_t xh = __float_as_uint(x) + 0x8000u, yh = __float_as_uint(y) + 0x8000u;
+  hi = __byte_perm(xh, yh, 0x7632);
+  const float xr = __fsub_rn(x, __uint_as_float(xh & kTop));
+  const float yr = __fsub_rn(y, __uint_as_float(yh & kTop));
+  const uint32_t xm = __float_as_uint(xr), ym = __float_as_uint(yr);
+  mid = __byte_perm(xm, ym, 0x7632);
+  lo = __byte_perm(__float_as_uint(__fsub_rn(xr, __uint_as_float(xm & kTop))),
+                   __float_as_uint(__fsub_rn(yr, __uint_as_float(ym & kTop))), 0x7632);
 }
 
 // Two adjacent 16 x 8 accumulator tiles as a 16 x 16 operand in three parts.
@@ -92,17 +100,15 @@ __device__ __forceinline__ void split_tiles(const float (&t0)[4], const float (&
 
 __device__ __forceinline__ void zero(float (&c)[4]) { c[0] = c[1] = c[2] = c[3] = 0.f; }
 
-// s = c s + d, two at a time.
+// s = c s + d (fp32x2 arithmetic keeps the matrix instructions waiting, see split2).
 __device__ __forceinline__ void scale_add(float (&s)[4], float c, const float (&d)[4]) {
-  const float2 cc = make_float2(c, c);
-  const float2 lo = __ffma2_rn(cc, make_float2(s[0], s[1]), make_float2(d[0], d[1]));
-  const float2 hi = __ffma2_rn(cc, make_float2(s[2], s[3]), make_float2(d[2], d[3]));
-  s[0] = lo.x; s[1] = lo.y; s[2] = hi.x; s[3] = hi.y;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) s[x] = fmaf(c, s[x], d[x]);
 }
 
 // The part pairs of a product, largest first: P operand parts of b (1: exact bf16, 3: split).
 // FULL leaves out none of the six (three with P = 1) that fp32 accuracy takes; without it the
-// pairs below 2^-16 go.
+// pairs below 2^-15 go.
 // Each pair is two digits, a's part and b's, in the packed lists.
 template <int P, bool FULL>
 struct Pairs {

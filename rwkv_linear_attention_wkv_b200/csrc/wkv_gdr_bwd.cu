@@ -21,7 +21,7 @@
 //
 // Rounding: the chain keeps the full three-part products everywhere (its results feed fp32
 // gradients of states), and so does the second kernel for fp32 problems and in whatever leads to
-// dg. What only the bf16 dq and dk see takes two parts (2^-17 a factor).
+// dg. What only the bf16 dk sees takes two parts (2^-15 a factor).
 #include <type_traits>
 
 #include "wkv_gdr.cuh"

@@ -92,7 +92,9 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
         }
         split_tiles(S[c / 8], S[c / 8 + 1], parts);
         mma_pairs<P, true>(xm, xc, parts, kb);
-        if (!SUMMARY) mma_pairs<P, !X::kBf16>(om, oc, parts, qb);
+        // (one sum where only a bf16 y sees it: 8 registers less)
+        if constexpr (!SUMMARY && X::kBf16) mma_up<P, false>(om, parts, qb);
+        if constexpr (!SUMMARY && !X::kBf16) mma_pairs<P, true>(om, oc, parts, qb);
       }
       // e: V^T - C_i X as accumulator, plus its product with (I + A)^-1 - I
       float e[2][4], ec[2][4];
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
         const float2 f = *reinterpret_cast<const float2*>(m.write + n * 8 + 2 * t4);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          o[n][x] = fmaf((x & 1) ? d.y : d.x, om[n][x] + oc[n][x], o[n][x]);
+          o[n][x] = fmaf((x & 1) ? d.y : d.x, X::kBf16 ? om[n][x] : om[n][x] + oc[n][x], o[n][x]);
           w[n][x] = e[n][x] * ((x & 1) ? f.y : f.x);
         }
       }
