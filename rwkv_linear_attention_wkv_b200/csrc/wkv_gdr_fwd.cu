@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
       float o[2][4];
       zero(o[0]);
       zero(o[1]);
-      mma_up<3, !X::kBf16>(o, ep, fb);
+      if (!SUMMARY) mma_up<3, !X::kBf16>(o, ep, fb);
       float w[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
