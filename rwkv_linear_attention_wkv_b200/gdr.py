@@ -65,13 +65,17 @@ def _run(fn, index, stream, *args):
         raise WkvError(fn.__name__, rc)
 
 
-def _scratch(nbytes, index, stream):
-    """Uninitialised bytes for one call: on another stream than the current one they stay taken
-    until that stream has passed the call."""
-    t = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+def _on(t, stream):
+    """t, made here for a call on `stream` (None: the current one): its memory stays taken until
+    that stream has passed the call, however soon the caller lets go of it."""
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+def _scratch(nbytes, index, stream):
+    """Uninitialised bytes for one call."""
+    return _on(torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index)), stream)
 
 
 def _bytes(fn, problem, index):
@@ -125,7 +129,7 @@ def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_sta
     p, index = _problem(q, v, 2, scale, seq_offsets)
     _inputs(q, k, v, g, beta, index)
     if y is None:
-        y = torch.empty_like(v)
+        y = _on(torch.empty_like(v), stream)
     else:
         _need(y, "y", v.dtype, v.shape, index)
     B, T, H, N = v.shape
@@ -135,7 +139,7 @@ def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_sta
     if not want_state:
         state_out = None
     elif state_out is None:
-        state_out = v.new_empty(states, dtype=_F32)
+        state_out = _on(v.new_empty(states, dtype=_F32), stream)
     else:
         _need(state_out, "state_out", _F32, states, index)
     scratch = None
@@ -210,6 +214,8 @@ def wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=None, scale=1.0
                  "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
         if want_dstate:
             grads["dstate"] = v.new_empty(states, dtype=_F32)
+        for t in grads.values():
+            _on(t, stream)
     else:
         for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
             _need(grads.get(n), n, t.dtype, t.shape, index)
@@ -253,7 +259,7 @@ def wkv_gdr_decode_step(q, k, v, g, beta, state, slots=None, scale=1.0, y=None, 
     elif n_slots < n:
         raise ValueError(f"state must have at least {n} slots, got {n_slots}")
     if y is None:
-        y = torch.empty_like(v)
+        y = _on(torch.empty_like(v), stream)
     else:
         _need(y, "y", v.dtype, v.shape, index)
     _run(lib.wkv_gdr_decode_step, index, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(),

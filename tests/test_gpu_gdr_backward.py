@@ -215,3 +215,26 @@ def test_backward_refusals(W):
         W.wkv_gdr_backward(*x, y, ws, scratch=ws[:100])
     with pytest.raises(TypeError, match="dq must be"):
         W.wkv_gdr_backward(*x, y, ws, grads={})
+
+
+def test_backward_on_a_given_stream_keeps_its_memory(W):
+    # the call waits behind other work on `side`; what the binding allocated for it must not be
+    # handed out on the current stream meanwhile
+    x = cuda(*ref.inputs((1, 1100), 1, 1, 64, BF16, 71))
+    dy = normal((1, 1100, 1, 64), 72, BF16).cuda()
+    y, S, ws = W.wkv_gdr_forward_checkpointed(*x)
+    want = W.wkv_gdr_backward(*x, dy, ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(10_000_000)
+    y2, S2, ws2 = W.wkv_gdr_forward_checkpointed(*x, stream=side)
+    got = W.wkv_gdr_backward(*x, dy, ws2, stream=side)
+    sizes = (ws2.numel(), 2 * ws2.numel(), 40 * 64 * 64)
+    del ws2
+    for n in sizes:
+        [torch.full((n // 4,), 1e30, device="cuda") for _ in range(4)]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(y2, y) and torch.equal(S2, S)
+    assert all(torch.equal(got[n], want[n]) for n in want)
