@@ -1,4 +1,5 @@
-"""Builds libwkv.so (the CUDA library behind include/wkv.h) in this package directory.
+"""Builds libwkv.so (the CUDA library behind include/wkv.h) and _binding.so (the short way into
+it from Python) in this package directory.
 
     python rwkv_linear_attention_wkv_b200/build.py [--verbose-ptxas] [--force]
 
@@ -6,22 +7,28 @@
 import the package, which needs the library this builds.)
 
 nvcc compiles every csrc/*.cu for sm_100a only and links one shared library with the
-CUDA runtime linked statically, so loading it needs no GPU and no torch.
+CUDA runtime linked statically, so loading it needs no GPU and no torch. _binding.so is compiled
+against the headers of the installed torch (found without importing it).
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libwkv.so")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CXX = os.environ.get("CXX", "g++")
 
 
 def sources():
@@ -45,7 +52,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return LIB
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
            "-std=c++17", "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
-           "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp"]
+           "--expt-relaxed-constexpr", "--threads", "0", "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp"]
     if verbose_ptxas:
         cmd += ["-Xptxas", "-v"]
     cmd += sources()
@@ -54,6 +61,24 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     return LIB
 
 
+def build_binding(force: bool = False) -> str:
+    """After build(): it links against the library."""
+    newest = max(os.path.getmtime(p) for p in
+                 [BINDING_SOURCE] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    subprocess.check_call(
+        [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+         "-I", os.path.join(torch, "include"), "-I", os.path.join(cuda, "include"),
+         "-I", sysconfig.get_paths()["include"], BINDING_SOURCE, "-o", BINDING + ".tmp",
+         "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+         "-L" + HERE, "-l:libwkv.so", "-Wl,-rpath,$ORIGIN"])
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
-    build(force=True, verbose_ptxas="--verbose-ptxas" in sys.argv)
-    print(LIB)
+    print(build(force=True, verbose_ptxas="--verbose-ptxas" in sys.argv))
+    print(build_binding(force=True))

@@ -2,6 +2,9 @@
 
 The tensors of a call must be on one device; the call runs there, on that device's current
 stream (or the stream given), whichever device is current.
+
+An ordinary call on the current stream goes through _binding.so (csrc/binding.cpp), which returns
+NotImplemented for whatever it does not take; the functions here then check, explain and call.
 """
 from __future__ import annotations
 
@@ -9,7 +12,13 @@ import ctypes
 
 import torch
 
-from . import WkvError, lib
+from . import LIB_PATH, WkvError, lib
+
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError(f"{LIB_PATH[:-len('libwkv.so')]}_binding.so is missing or older than torch: "
+                      "build it with `python rwkv_linear_attention_wkv_b200/build.py`") from e
 
 _F32 = torch.float32
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -160,6 +169,11 @@ def wkv_gdr_forward(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None, y
     N, N) fp32 or None (zero). Returns (y, S_T), or (y, None) with want_state=False. state_out
     may be `state` itself.
     """
+    if stream is None:
+        done = _binding.gdr_forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out,
+                                    want_state)
+        if done is not NotImplemented:
+            return done
     p, y, s1, index, _held = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out,
                                       want_state, stream)
     _run(lib.wkv_gdr_forward, index, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -184,6 +198,11 @@ def wkv_gdr_forward_checkpointed(q, k, v, g, beta, state=None, scale=1.0, seq_of
     """wkv_gdr_forward that also keeps what wkv_gdr_backward reads. Returns (y, S_T, workspace);
     hand the workspace (it is only read there) to the backward of the same inputs. seq_offsets
     must not decrease. state_out must not be `state` if `state` is needed again."""
+    if stream is None:
+        done = _binding.gdr_forward_checkpointed(q, k, v, g, beta, state, scale, seq_offsets, y,
+                                                 state_out, want_state, workspace)
+        if done is not NotImplemented:
+            return done
     p, y, s1, index, _held = _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out,
                                       want_state, stream)
     nbytes = int(lib.wkv_gdr_checkpoint_bytes(ctypes.byref(p)))
@@ -202,6 +221,11 @@ def wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=None, scale=1.0
 
     grads: such a dict to write into. Rows of the gradients that no packed sequence covers are
     left as they were (uninitialised without `grads`)."""
+    if stream is None and grads is None and scratch is None:
+        done = _binding.gdr_backward(q, k, v, g, beta, dy, workspace, grad_state, scale,
+                                     seq_offsets, want_dstate)
+        if done is not NotImplemented:
+            return done
     p, index = _problem(q, v, 2, scale, seq_offsets)
     _inputs(q, k, v, g, beta, index)
     _need(dy, "dy", v.dtype, v.shape, index)
@@ -246,6 +270,10 @@ def wkv_gdr_decode_step(q, k, v, g, beta, state, slots=None, scale=1.0, y=None, 
     (no slot twice; outside [0, len(state)): padding, the row is skipped and its y stays as it
     was), None = row i has state i. Returns y (n, H, N).
     """
+    if stream is None:
+        done = _binding.gdr_decode(q, k, v, g, beta, state, slots, scale, y)
+        if done is not NotImplemented:
+            return done
     p, index = _problem(q, v, 1, scale)
     _inputs(q, k, v, g, beta, index)
     n, H, N = v.shape

@@ -1,6 +1,7 @@
 """Binding of the norms around a block (include/wkv.h, wkv_norm_gate_*): argument marshalling only.
 
-As in gdr.py, the tensors of a call must be on one device, and the call runs there.
+As in gdr.py, the tensors of a call must be on one device, and the call runs there; ordinary calls
+go through _binding.so.
 """
 from __future__ import annotations
 
@@ -9,7 +10,7 @@ import ctypes
 import torch
 
 from . import lib
-from .gdr import _DTYPES, _F32, _at, _buffer, _need, _on, _run
+from .gdr import _binding, _DTYPES, _F32, _at, _buffer, _need, _on, _run
 
 _ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
 
@@ -56,6 +57,11 @@ def wkv_norm_gate_forward(h, weight=None, gate=None, x=None, scale=None, next_we
     scale, next_weight: fp32 (C,). gate (with act="none"), weight, x, scale and next_weight may
     be left out. group: default C. Returns (out, y), y None without next_weight; `out` may be h
     or x itself."""
+    if stream is None:
+        done = _binding.norm_gate_forward(h, weight, gate, x, scale, next_weight, group, act, eps,
+                                          out, y)
+        if done is not NotImplemented:
+            return done
     p, index = _problem(h, weight, gate, x, scale, next_weight, group, act, eps)
     dt = h.dtype
     if out is None:
@@ -83,6 +89,11 @@ def wkv_norm_gate_backward(h, weight, dout, gate=None, x=None, scale=None, next_
     """Gradients of sum(dout * out) + sum(dy * y) for wkv_norm_gate_forward's (out, y). dout or dy
     may be None (zero). Returns a dict of dh, dgate, dx (as h) and dweight, dscale, dnext_weight
     (fp32), None where the forward had no such input (dnext_weight also without dy)."""
+    if stream is None and workspace is None:
+        done = _binding.norm_gate_backward(h, weight, dout, gate, x, scale, next_weight, dy, group,
+                                           act, eps)
+        if done is not NotImplemented:
+            return done
     if dout is None and dy is None:
         raise ValueError("dout or dy must be given")
     if dy is not None and next_weight is None:
