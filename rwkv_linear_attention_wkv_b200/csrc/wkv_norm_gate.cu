@@ -113,11 +113,31 @@ __device__ __forceinline__ Eight params(const float* row, const Place<VEC>& pl) 
   }
   return x;
 }
+// The three weights' rows, ones where there is none, zeros past C.
 template <bool VEC>
-__device__ __forceinline__ void put_params(float* row, const float* p, int step, int C) {
-  for (int c = threadIdx.x; c < kE * step; c += blockDim.x) {
-    const int to = VEC ? (c % kE / 4) * 4 * step + c / kE * 4 + c % 4 : c;
-    row[to] = c >= C ? 0.f : p ? p[c] : 1.f;
+__device__ __forceinline__ void put_params(float* rows, const float* w, const float* s,
+                                           const float* n, int step, int C) {
+  for (int i = threadIdx.x; i < 3 * step; i += blockDim.x) {
+    const int j = i / step, at = i % step;
+    const float* const p = j == 0 ? w : j == 1 ? s : n;
+    float* const row = rows + j * kE * step;
+    if (VEC && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (at * kE < C)
+          v = p ? *reinterpret_cast<const float4*>(p + at * kE + 4 * half)
+                : make_float4(1.f, 1.f, 1.f, 1.f);
+        *reinterpret_cast<float4*>(row + half * 4 * step + 4 * at) = v;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const int c = VEC ? at * kE + e : e * step + at;
+        const int to = VEC ? e / 4 * 4 * step + 4 * at + e % 4 : c;
+        row[to] = c >= C ? 0.f : p ? p[c] : 1.f;
+      }
+    }
   }
 }
 
@@ -242,10 +262,6 @@ __global__ void __launch_bounds__(MAX_THREADS, fwd_ctas(sizeof(T) == 2, MAX_THRE
   make_team<VEC>(team_warps, a.C, t, pl);
   const int teams = (blockDim.x >> 5) / team_warps;
   const int wide = pl.step * kE;
-  put_params<VEC>(t.weights, a.weight, pl.step, a.C);
-  put_params<VEC>(t.weights + wide, a.scale, pl.step, a.C);
-  put_params<VEC>(t.weights + 2 * wide, a.next_weight, pl.step, a.C);
-  __syncthreads();
   const T *h = static_cast<const T*>(a.h), *z = static_cast<const T*>(a.gate),
           *x = static_cast<const T*>(a.x);
   const float inv_group = 1.f / a.group, inv_c = 1.f / a.C;
@@ -258,6 +274,8 @@ __global__ void __launch_bounds__(MAX_THREADS, fwd_ctas(sizeof(T) == 2, MAX_THRE
     if (x) xr = load_raw<T, VEC>(x + r * a.C, pl);
   };
   if (row < a.R) fetch(row);
+  put_params<VEC>(t.weights, a.weight, a.scale, a.next_weight, pl.step, a.C);
+  __syncthreads();
   for (; row < a.R; row += stride) {
     const Eight hv = widen<T>(hr);
     Eight m = params<VEC>(t.weights, pl);
@@ -306,10 +324,6 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_bwd_kernel(NormGateA
   make_team<VEC>(team_warps, a.C, t, pl);
   const int teams = (blockDim.x >> 5) / team_warps;
   const int wide = pl.step * kE;
-  put_params<VEC>(t.weights, a.weight, pl.step, a.C);
-  put_params<VEC>(t.weights + wide, a.scale, pl.step, a.C);
-  put_params<VEC>(t.weights + 2 * wide, a.next_weight, pl.step, a.C);
-  __syncthreads();
   const T *h = static_cast<const T*>(a.h), *z = static_cast<const T*>(a.gate),
           *x = static_cast<const T*>(a.x), *dout = static_cast<const T*>(a.dout),
           *dy = static_cast<const T*>(a.dy);
@@ -326,6 +340,8 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_bwd_kernel(NormGateA
     if (dy) dyr = load_raw<T, VEC>(dy + r * a.C, pl);
   };
   if (first < a.R) fetch(first);
+  put_params<VEC>(t.weights, a.weight, a.scale, a.next_weight, pl.step, a.C);
+  __syncthreads();
   for (int64_t row = first; row < a.R; row += stride) {
     Eight hn = widen<T>(hr), sig{}, d{}, out{};
     const Raw<T> zk = zr;
@@ -418,10 +434,11 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_bwd_kernel(NormGateA
     for (int j = 0; j < 3; ++j) line[j * a.C + c] = sums[j * wide + c];
 }
 
-// The CTAs' lines added up: 32 columns x 8 slices of the lines a CTA, the slices in order.
-__global__ void __launch_bounds__(256) norm_gate_sum_kernel(const float* partial, int lines, int C,
-                                                            float* dw, float* ds, float* dwn) {
-  __shared__ float part[8][32];
+// The CTAs' lines added up: 32 columns x kSlices slices of the lines a CTA, the slices in order.
+constexpr int kSlices = 16;
+__global__ void __launch_bounds__(32 * kSlices)
+    norm_gate_sum_kernel(const float* partial, int lines, int C, float* dw, float* ds, float* dwn) {
+  __shared__ float part[kSlices][32];
   float* const to = blockIdx.y == 0 ? dw : blockIdx.y == 1 ? ds : dwn;
   if (to == nullptr) return;
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
@@ -430,12 +447,12 @@ __global__ void __launch_bounds__(256) norm_gate_sum_kernel(const float* partial
   if (c < C) {
     const float* p = partial + int64_t(blockIdx.y) * C + c;
 #pragma unroll 8
-    for (int l = slice; l < lines; l += 8) s += p[int64_t(l) * 3 * C];
+    for (int l = slice; l < lines; l += kSlices) s += p[int64_t(l) * 3 * C];
   }
   part[slice][lane] = s;
   __syncthreads();
   if (slice == 0 && c < C) {
-    for (int i = 1; i < 8; ++i) s += part[i][lane];
+    for (int i = 1; i < kSlices; ++i) s += part[i][lane];
     to[c] = s;
   }
 }
@@ -541,7 +558,7 @@ int launch_norm_gate_backward(const NormGateArgs& a, cudaStream_t stream) {
                         : pick<float>(a, p, vec, true, stream);
   if (rc != WKV_OK) return rc;
   if (!a.dweight && !a.dscale && !a.dnext_weight) return WKV_OK;
-  norm_gate_sum_kernel<<<dim3((a.C + 31) / 32, 3), 256, 0, stream>>>(
+  norm_gate_sum_kernel<<<dim3((a.C + 31) / 32, 3), 32 * kSlices, 0, stream>>>(
       a.partial, p.grid, a.C, a.dweight, a.dscale, a.dnext_weight);
   return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
 }
