@@ -212,6 +212,11 @@ __device__ __forceinline__ int by_length(const GdrArgs& a, int rank, int lane) {
   return lo != 0 ? __ffs(lo) - 1 : 31 + __ffs(hi);
 }
 
+// Segments of a sequence: none of up to three, which three passes would not gain anything.
+__device__ __forceinline__ int spans_of(int len, int tokens) {
+  return len <= 3 * int64_t(tokens) ? 1 : (len - 1) / tokens + 1;
+}
+
 // What a CTA walks: a sequence, or segment `s` of its `count`.
 struct Span {
   int seq, s, count, slot;
@@ -230,9 +235,8 @@ __device__ __forceinline__ bool find_span(const GdrArgs& a, const GdrSegs& g, in
     sp.t_seq = sp.t0 = sequence(a, sp.seq, sp.len);
     return true;
   }
-  auto count_of = [&](int len) { return len <= g.tokens ? 1 : (len - 1) / g.tokens + 1; };
   if (a.offsets == nullptr) {
-    sp.count = count_of(a.T);
+    sp.count = spans_of(a.T, g.tokens);
     sp.seq = index / sp.count;
     sp.s = index % sp.count;
   } else {  // up to 64 sequences
@@ -242,7 +246,7 @@ __device__ __forceinline__ bool find_span(const GdrArgs& a, const GdrSegs& g, in
       int len = 0;
       if (p * 32 + lane < a.n_seqs) {
         sequence(a, p * 32 + lane, len);
-        count[p] = count_of(len);
+        count[p] = spans_of(len, g.tokens);
       }
       upto[p] = count[p];
 #pragma unroll
@@ -269,7 +273,7 @@ __device__ __forceinline__ bool find_span(const GdrArgs& a, const GdrSegs& g, in
   int len;
   sp.t_seq = sequence(a, sp.seq, len);
   sp.t0 = sp.t_seq + int64_t(sp.s) * g.tokens;
-  sp.len = min(len - sp.s * g.tokens, g.tokens);
+  sp.len = sp.count == 1 ? len : min(len - sp.s * g.tokens, g.tokens);
   return true;
 }
 

@@ -193,7 +193,7 @@ WKV_API int wkv_gdr_decode_step(const wkv_gdr_problem* p, const void* q, const v
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.y = y; a.s0 = state; a.s1 = state;
   a.n_slots = int(n_slots);
   a.slots = slots;
-  return launch_gdr_recurrent(a, stream);
+  return launch_gdr_decode(a, stream);
 }
 
 }  // extern "C"

@@ -161,8 +161,8 @@ struct GdrArgs {
   int n_slots = 0;
   const int32_t* slots = nullptr;
 };
-// Token by token, the state in registers.
-int launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream);
+// One token a row, the states in place.
+int launch_gdr_decode(const GdrArgs& a, cudaStream_t stream);
 // Walks in segments, side by side, where a few heads would leave most SMs idle (wkv_gdr_seg.cu).
 // A state leaves a segment as S M + B, M and B from the segment's tokens alone.
 struct GdrSegs {

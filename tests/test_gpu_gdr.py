@@ -145,9 +145,9 @@ def test_forward_in_segments_strong_decays_and_state_in_place(W, N):
 
 @pytest.mark.parametrize("N", [64, 128])
 def test_forward_packed_in_segments(W, N):
-    # one sequence of several segments, one of exactly two, one of one, an empty one
+    # one sequence long enough for segments, two that are walked whole, an empty one
     off = [3, 3, 1000, 1512, 1600]
-    T, H = 1700, 2
+    T, H = 2100, 2
     x = ref.inputs((1, T), 1, H, N, BF16, 25)
     S0 = states(4, H, N, 26)
     y = torch.full((1, T, H, N), 7.0, dtype=BF16, device="cuda")

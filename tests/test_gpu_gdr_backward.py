@@ -138,7 +138,7 @@ def test_backward_in_segments(W, N, B, T, Hk, H, dtype):
 @pytest.mark.parametrize("N", [64, 128])
 def test_backward_packed_in_segments(W, N):
     off = [3, 3, 1000, 1512, 1600]
-    T, H, n = 1700, 1, 4
+    T, H, n = 2100, 1, 4
     x = ref.inputs((1, T), 1, H, N, FP32, 27)
     dy = normal((1, T, H, N), 28)
     S0, dS = 0.3 * normal((n, H, N, N), 29), 0.3 * normal((n, H, N, N), 30)
