@@ -235,7 +235,7 @@ __device__ __forceinline__ Eight group_sum(const Eight& x, Team& t, const Place<
 // the sigmoid by at most s (1 - s) |z| 2^-24 < 2^-26. (expf and a division: 15 instructions more,
 // a third of a forward row.)
 __device__ __forceinline__ float sigmoid_of(float z) {
-  return __fdividef(1.f, 1.f + ex2(z * -1.4426950408889634f));
+  return rcp(1.f + ex2(z * -1.4426950408889634f));
 }
 
 template <bool VEC>
@@ -287,9 +287,10 @@ __global__ void __launch_bounds__(MAX_THREADS, fwd_ctas(sizeof(T) == 2, MAX_THRE
     if (z) {
       const Eight zv = widen<T>(zr);
 #pragma unroll
-      for (int i = 0; i < kE; ++i) {
-        const float sig = sigmoid_of(zv.v[i]);
-        m.v[i] *= a.act == WKV_ACT_SILU ? zv.v[i] * sig : sig;
+      for (int i = 0; i < kE; ++i) m.v[i] *= sigmoid_of(zv.v[i]);
+      if (a.act == WKV_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < kE; ++i) m.v[i] *= zv.v[i];
       }
     }
     Eight xv{};
