@@ -71,15 +71,17 @@ __device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Two values as three packed bf16 parts that add up to them: hi to the nearest, mid and lo by
-// cutting off (8 bits each). With integer adds, masks and byte permutes: packed conversions and
+// Two values as three packed bf16 parts that add up to them, 8 bits each: mid and lo by cutting
+// off, hi to the nearest, or cut off as well (CUT: two instructions less, for operands of a product
+// with exact bf16 values, where no part pair is left out; two parts are then good to 2^-15). With integer adds, masks and byte permutes: packed conversions and
 // fp32x2 arithmetic take as many instructions, but wait for one another and for the matrix
 // instructions (16 such splits beside 16 matrix instructions, cycles a scheduler: 435 with
 // conversions, 298 this way; 129 for the matrix instructions alone).
+template <bool CUT = false>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& mid,
                                        uint32_t& lo) {
-  constexpr uint32_t kTop = 0xffff0000u;
-  const uint32_t xh = __float_as_uint(x) + 0x8000u, yh = __float_as_uint(y) + 0x8000u;
+  constexpr uint32_t kTop = 0xffff0000u, kHalf = CUT ? 0u : 0x8000u;
+  const uint32_t xh = __float_as_uint(x) + kHalf, yh = __float_as_uint(y) + kHalf;
   hi = __byte_perm(xh, yh, 0x7632);
   const float xr = __fsub_rn(x, __uint_as_float(xh & kTop));
   const float yr = __fsub_rn(y, __uint_as_float(yh & kTop));
@@ -90,12 +92,13 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 }
 
 // Two adjacent 16 x 8 accumulator tiles as a 16 x 16 operand in three parts.
+template <bool CUT = false>
 __device__ __forceinline__ void split_tiles(const float (&t0)[4], const float (&t1)[4],
                                             uint32_t (&a)[3][4]) {
-  split2(t0[0], t0[1], a[0][0], a[1][0], a[2][0]);
-  split2(t0[2], t0[3], a[0][1], a[1][1], a[2][1]);
-  split2(t1[0], t1[1], a[0][2], a[1][2], a[2][2]);
-  split2(t1[2], t1[3], a[0][3], a[1][3], a[2][3]);
+  split2<CUT>(t0[0], t0[1], a[0][0], a[1][0], a[2][0]);
+  split2<CUT>(t0[2], t0[3], a[0][1], a[1][1], a[2][1]);
+  split2<CUT>(t1[0], t1[1], a[0][2], a[1][2], a[2][2]);
+  split2<CUT>(t1[2], t1[3], a[0][3], a[1][3], a[2][3]);
 }
 
 __device__ __forceinline__ void zero(float (&c)[4]) { c[0] = c[1] = c[2] = c[3] = 0.f; }

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
         uint32_t parts[3][4], kb[P][4];
 #pragma unroll
         for (int p = 0; p < P; ++p) ldsm4(kb[p], tile(i, 0, p) + to + c * 2);
-        split_tiles(S[c / 8], S[c / 8 + 1], parts);
+        split_tiles<X::kBf16>(S[c / 8], S[c / 8 + 1], parts);
         mma_pairs<P, true>(xm, xc, parts, kb);
       }
       // R^T
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
       }
       // dD = C dD + W1^T Q + W2^T K
       uint32_t bp[3][4];
-      split_tiles(w1[0], w1[1], ap);
-      split_tiles(w2[0], w2[1], bp);
+      split_tiles<X::kBf16>(w1[0], w1[1], ap);
+      split_tiles<X::kBf16>(w2[0], w2[1], bp);
       const float end = m.end;
       const uint32_t ch = at_channels(lane, X::kPitch) + grp;
 #pragma unroll
@@ -253,11 +253,11 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 }
 
 // One value as PARTS bf16 parts, four at a time, PART bytes apart.
-template <int PARTS, int PART>
+template <int PARTS, int PART, bool CUT>
 __device__ __forceinline__ void put_parts(unsigned char* d, float4 x) {
   uint2 p[3];
-  split2(x.x, x.y, p[0].x, p[1].x, p[2].x);
-  split2(x.z, x.w, p[0].y, p[1].y, p[2].y);
+  split2<CUT>(x.x, x.y, p[0].x, p[1].x, p[2].x);
+  split2<CUT>(x.z, x.w, p[0].y, p[1].y, p[2].y);
 #pragma unroll
   for (int i = 0; i < PARTS; ++i) *reinterpret_cast<uint2*>(d + i * PART) = p[i];
 }
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
         const int t = i / kQuads, c = (i % kQuads) * 4;
         const float4 x = t < len ? *reinterpret_cast<const float4*>(src + t * row + c)
                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-        put_parts<3, X::kTile>(smem + off + (t * X::kPitch + c) * 2, x);
+        put_parts<3, X::kTile, false>(smem + off + (t * X::kPitch + c) * 2, x);
       }
     }
   };
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
 #pragma unroll
       for (int x = 0; x < kSt; ++x) {
         const int i = threadIdx.x + x * X::kThreads;
-        put_parts<decltype(parts)::value, X::kState>(
+        put_parts<decltype(parts)::value, X::kState, X::kBf16>(
             smem + X::kOffS + (i / kQuads * X::kPitch + (i % kQuads) * 4) * 2, sr[x]);
       }
     };
@@ -494,9 +494,9 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
         if (t < len) b.dbeta[(t0 + t) * a.H + h] = s;
       }
       const int to = (t * X::kPitch + c) * 2;
-      put_parts<PA, X::kTile>(smem + X::kOffU + to,
+      put_parts<PA, X::kTile, X::kBf16>(smem + X::kOffU + to,
                               make_float4(be * e.x, be * e.y, be * e.z, be * e.w));
-      put_parts<PP, X::kTile>(smem + X::kOffDe + to,
+      put_parts<PP, X::kTile, X::kBf16>(smem + X::kOffDe + to,
                               make_float4(be * d.x, be * d.y, be * d.z, be * d.w));
     }
     const uint32_t rows = at_rows(lane, X::kPitch) + uint32_t(strip * 16 * X::kPitch) * 2u;
@@ -591,11 +591,11 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
         const float d1 = i >= j + 1 ? decay_between(ci, F.c[j + 1]) : 0.f;
         uint32_t p[3];
         const int to = (i * X::kPPitch + j) * 2;
-        split2(a.scale * d0 * pw[n][2 * z], a.scale * d1 * pw[n][2 * z + 1], p[0], p[1], p[2]);
+        split2<X::kBf16>(a.scale * d0 * pw[n][2 * z], a.scale * d1 * pw[n][2 * z + 1], p[0], p[1], p[2]);
 #pragma unroll
         for (int x = 0; x < PA; ++x)
           *reinterpret_cast<uint32_t*>(smem + X::kOffS + x * X::kPTile + to) = p[x];
-        split2(i > j ? d0 * zw[n][2 * z] : 0.f, i > j + 1 ? d1 * zw[n][2 * z + 1] : 0.f, p[0], p[1],
+        split2<X::kBf16>(i > j ? d0 * zw[n][2 * z] : 0.f, i > j + 1 ? d1 * zw[n][2 * z + 1] : 0.f, p[0], p[1],
                p[2]);
 #pragma unroll
         for (int x = 0; x < PP; ++x)

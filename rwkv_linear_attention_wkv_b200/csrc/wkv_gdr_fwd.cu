@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
           ldsm4(kb[p], tile(i, 0, p) + to + c * 2);
           if (!SUMMARY) ldsm4(qb[p], tile(i, 1, p) + to + c * 2);
         }
-        split_tiles(S[c / 8], S[c / 8 + 1], parts);
+        split_tiles<X::kBf16>(S[c / 8], S[c / 8 + 1], parts);
         mma_pairs<P, true>(xm, xc, parts, kb);
         // (one sum where only a bf16 y sees it: 8 registers less)
         if constexpr (!SUMMARY && X::kBf16) mma_up<P, false>(om, parts, qb);
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
       }
       // S = C S_0 + W^T K, the products summed on their own
       uint32_t wp[3][4];
-      split_tiles(w[0], w[1], wp);
+      split_tiles<X::kBf16>(w[0], w[1], wp);
       const float end = m.end;
       const uint32_t ch = at_channels(lane, X::kPitch) + grp;
 #pragma unroll
