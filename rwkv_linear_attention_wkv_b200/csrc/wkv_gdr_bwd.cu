@@ -243,11 +243,13 @@ struct Chunk {
   static constexpr int kSmem = kOffF + int(sizeof(Floats));
 };
 
-__device__ __forceinline__ float4 load4(const float* p) {
-  return *reinterpret_cast<const float4*>(p);
-}
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 r = *reinterpret_cast<const uint2*>(p);
+// Four values as they are in memory.
+template <typename T> struct Raw4;
+template <> struct Raw4<float> { typedef float4 Type; };
+template <> struct Raw4<__nv_bfloat16> { typedef uint2 Type; };
+template <typename T> using Four = typename Raw4<T>::Type;
+__device__ __forceinline__ float4 widen(const float4& x) { return x; }
+__device__ __forceinline__ float4 widen(const uint2& r) {
   const float2 lo = unpack(r.x), hi = unpack(r.y);
   return make_float4(lo.x, lo.y, hi.x, hi.y);
 }
@@ -328,7 +330,9 @@ __device__ __forceinline__ uint32_t at_rows(int lane, int pitch) {
   return uint32_t(((m & 1) * 8 + r) * pitch + (m >> 1) * 8) * 2u;
 }
 
-template <typename T, int N>
+// SHARED: several value heads share the query/key head, whose dq and dk are summed over them (32
+// more registers).
+template <typename T, int N, bool SHARED>
 __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     gdr_chunk_kernel(GdrBwdArgs b) {
   using X = Chunk<T, N>;
@@ -385,8 +389,8 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
 #pragma unroll 4
       for (int i = threadIdx.x; i < L * kQuads; i += X::kThreads) {
         const int t = i / kQuads, c = (i % kQuads) * 4;
-        const float4 x = t < len ? *reinterpret_cast<const float4*>(src + t * row + c)
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 x = *reinterpret_cast<const float4*>(src + min(t, len - 1) * row + c);
+        if (t >= len) x = make_float4(0.f, 0.f, 0.f, 0.f);
         put_parts<3, X::kTile, false>(smem + off + (t * X::kPitch + c) * 2, x);
       }
     }
@@ -419,26 +423,44 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     }
   };
 
-  float dq[NT][4], dk[NT][4];  // sums over the value heads
+  auto put_rows = [&](void* to, const float(&x)[NT][4]) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) zero(dq[n]), zero(dk[n]);
+    for (int z = 0; z < 2; ++z) {
+      const int t = strip * 16 + g4 + z * 8;
+      if (t >= len) continue;
+      T* const row =
+          static_cast<T*>(to) + (t0 + t) * qk_row + int64_t(hk) * N + slice * X::kCols + 2 * t4;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float2 v = make_float2(x[n][2 * z], x[n][2 * z + 1]);
+        if constexpr (X::kBf16)
+          *reinterpret_cast<__nv_bfloat162*>(row + n * 8) = __float22bfloat162_rn(v);
+        else
+          *reinterpret_cast<float2*>(row + n * 8) = v;
+      }
+    }
+  };
+
+  float dq[SHARED ? NT : 1][4], dk[SHARED ? NT : 1][4];  // sums over the value heads
+#pragma unroll
+  for (int n = 0; n < (SHARED ? NT : 1); ++n) zero(dq[n]), zero(dk[n]);
 
 #pragma unroll 1
   for (int h = hk * G; h < hk * G + G; ++h) {
     const int64_t state_at = (slot * a.H + h) * N * N;
     // what the head needs first, on its way before anything is waited for
     constexpr int kTok = L * kQuads / X::kThreads, kSt = X::kRows * kQuads / X::kThreads;
-    float4 er[kTok], dr[kTok], vr[kTok], sr[kSt];
+    float4 er[kTok], dr[kTok], sr[kSt];
+    Four<T> vr[kTok];
+    // (rows past the end read the last one: a branch would put the loads one after the other)
 #pragma unroll
     for (int x = 0; x < kTok; ++x) {
-      const int i = threadIdx.x + x * X::kThreads, t = i / kQuads;
-      const int64_t at = (t0 + t) * v_row + int64_t(h) * N + (i % kQuads) * 4;
-      er[x] = dr[x] = vr[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < len) {
-        er[x] = *reinterpret_cast<const float4*>(b.e + at);
-        dr[x] = *reinterpret_cast<const float4*>(b.du + at);
-        vr[x] = load4(static_cast<const T*>(a.v) + at);
-      }
+      const int i = threadIdx.x + x * X::kThreads;
+      const int64_t at =
+          (t0 + min(i / kQuads, len - 1)) * v_row + int64_t(h) * N + (i % kQuads) * 4;
+      er[x] = *reinterpret_cast<const float4*>(b.e + at);
+      dr[x] = *reinterpret_cast<const float4*>(b.du + at);
+      vr[x] = *reinterpret_cast<const Four<T>*>(static_cast<const T*>(a.v) + at);
     }
     // 64 rows of a state, from global memory and into parts
     auto fetch_state = [&](const float* src, int r0) {
@@ -480,7 +502,9 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
 #pragma unroll
     for (int x = 0; x < kTok; ++x) {
       const int i = threadIdx.x + x * X::kThreads, t = i / kQuads, c = (i % kQuads) * 4;
-      const float4 e = er[x], d = dr[x], v = vr[x];
+      const bool in = t < len;
+      const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 e = in ? er[x] : zero4, d = in ? dr[x] : zero4, v = in ? widen(vr[x]) : zero4;
       const float be = F.beta[t];
       float s = fmaf(e.x, d.x, fmaf(e.y, d.y, fmaf(e.z, d.z, e.w * d.w)));
       float w = fmaf(v.x, d.x, fmaf(v.y, d.y, fmaf(v.z, d.z, v.w * d.w)));
@@ -491,7 +515,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
       }
       if (c == 0) {
         F.written[t] = be * w;
-        if (t < len) b.dbeta[(t0 + t) * a.H + h] = s;
+        if (in) b.dbeta[(t0 + t) * a.H + h] = s;
       }
       const int to = (t * X::kPitch + c) * 2;
       put_parts<PA, X::kTile, X::kBf16>(smem + X::kOffU + to,
@@ -624,9 +648,16 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        dq[n][x] += q1[n][x];
-        dk[n][x] += k2[n][x] - k1[n][x];
+        k2[n][x] -= k1[n][x];
+        if constexpr (SHARED) {
+          dq[n][x] += q1[n][x];
+          dk[n][x] += k2[n][x];
+        }
       }
+    if constexpr (!SHARED) {
+      put_rows(b.dq, q1);
+      put_rows(b.dk, k2);
+    }
     __syncthreads();
     if (warp == 0) {
       // dg: the sums over later tokens of the chunk, on top of <dD, S_L>
@@ -650,25 +681,9 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     }
   }
 
-#pragma unroll
-  for (int z = 0; z < 2; ++z) {
-    const int t = strip * 16 + g4 + z * 8;
-    if (t >= len) continue;
-    const int64_t at = (t0 + t) * qk_row + int64_t(hk) * N + slice * X::kCols + 2 * t4;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if constexpr (X::kBf16) {
-        *reinterpret_cast<__nv_bfloat162*>(static_cast<T*>(b.dq) + at + n * 8) =
-            __float22bfloat162_rn(make_float2(dq[n][2 * z], dq[n][2 * z + 1]));
-        *reinterpret_cast<__nv_bfloat162*>(static_cast<T*>(b.dk) + at + n * 8) =
-            __float22bfloat162_rn(make_float2(dk[n][2 * z], dk[n][2 * z + 1]));
-      } else {
-        *reinterpret_cast<float2*>(static_cast<T*>(b.dq) + at + n * 8) =
-            make_float2(dq[n][2 * z], dq[n][2 * z + 1]);
-        *reinterpret_cast<float2*>(static_cast<T*>(b.dk) + at + n * 8) =
-            make_float2(dk[n][2 * z], dk[n][2 * z + 1]);
-      }
-    }
+  if constexpr (SHARED) {
+    put_rows(b.dq, dq);
+    put_rows(b.dk, dk);
   }
 }
 
@@ -692,7 +707,8 @@ int chain(const GdrBwdArgs& b, const GdrSegs& segs, cudaStream_t stream) {
 template <typename T, int N>
 int rest(const GdrBwdArgs& b, cudaStream_t stream) {
   using X = Chunk<T, N>;
-  auto* kernel = gdr_chunk_kernel<T, N>;
+  auto* kernel =
+      b.p.H == b.p.Hk ? gdr_chunk_kernel<T, N, false> : gdr_chunk_kernel<T, N, true>;
   if (!allow_smem(kernel, X::kSmem)) return WKV_ERR_CUDA;
   kernel<<<unsigned(gdr_chunks(b.p) * b.p.Hk), X::kThreads, X::kSmem, stream>>>(b);
   return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
