@@ -643,10 +643,10 @@ __device__ __forceinline__ bool start_state(float (&S)[N / 8][4], const GdrArgs&
 
 // Four consumers and steps of two groups everywhere (heads of 128 are two CTAs). bf16: two
 // producers, 168 registers and two CTAs an SM where there is work for them, or four producers and
-// one CTA, which is quicker alone (us, singles / pairs: 1 x 2048 x 8 x 64: 134 / 121, 1 x 2048 x 8
-// x 128: 210 / 178) and slower where CTAs queue (8 x 4096 x 64 x 64: 821 / 937, 16 x 1024 x 32 x
-// 128: 582 / 618). fp32 splits q and k on the way, which takes four producers always (8 x 1024 x
-// 64 x 64: 496 / 388, 1 x 2048 x 8 x 64: 253 / 194).
+// one CTA, which is quicker alone (us, singles / pairs: 1 x 2048 x 8 x 64: 129 / 114, 1 x 2048 x 8
+// x 128: 199 / 168) and slower where CTAs queue (8 x 4096 x 64 x 64: 785 / 881, 16 x 1024 x 32 x
+// 128: 561 / 599). fp32 splits q and k on the way, which takes four producers always (two / four:
+// 8 x 1024 x 64 x 64: 496 / 379, 1 x 2048 x 8 x 64: 253 / 186).
 enum GdrWalkForm { kGdrWalkSingles, kGdrWalkPairs, kGdrWalkError };
 inline GdrWalkForm gdr_walk_form(const GdrArgs& a, int64_t spans) {
   int dev = 0, sms = 0;

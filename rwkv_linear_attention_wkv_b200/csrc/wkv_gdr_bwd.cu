@@ -23,7 +23,7 @@
 // gradients of states), and so does the second kernel for fp32 problems and in whatever leads to
 // dg. What only the bf16 dk sees takes two parts (2^-15 a factor).
 //
-// Measured, 16 x 1024 x 12 x 64 bf16: chain 120 us, second kernel 203 us. The chain is bound like
+// Measured, 16 x 1024 x 12 x 64 bf16: chain 122 us, second kernel 196 us. The chain is bound like
 // the forward (wkv_gdr_fwd.cu). The second kernel issues a third of the time and has its matrix
 // pipe busy a quarter: 16 warps an SM wait for each other's tiles (barriers) and for e, du and
 // states, 2 KB a token and head, which HBM delivers in 55 us.
