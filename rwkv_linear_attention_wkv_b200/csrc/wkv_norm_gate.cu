@@ -40,6 +40,46 @@ struct Eight {
   float v[kE];
 };
 
+// Eight at a time, two to an instruction.
+__device__ __forceinline__ float2 two(const Eight& a, int i) {
+  return make_float2(a.v[2 * i], a.v[2 * i + 1]);
+}
+__device__ __forceinline__ void put(Eight& a, int i, float2 x) {
+  a.v[2 * i] = x.x;
+  a.v[2 * i + 1] = x.y;
+}
+__device__ __forceinline__ Eight operator*(const Eight& a, const Eight& b) {
+  Eight r;
+#pragma unroll
+  for (int i = 0; i < kE / 2; ++i) put(r, i, __fmul2_rn(two(a, i), two(b, i)));
+  return r;
+}
+__device__ __forceinline__ Eight operator*(const Eight& a, float b) {
+  Eight r;
+#pragma unroll
+  for (int i = 0; i < kE / 2; ++i) put(r, i, __fmul2_rn(two(a, i), make_float2(b, b)));
+  return r;
+}
+__device__ __forceinline__ Eight fma(const Eight& a, const Eight& b, const Eight& c) {
+  Eight r;
+#pragma unroll
+  for (int i = 0; i < kE / 2; ++i) put(r, i, __ffma2_rn(two(a, i), two(b, i), two(c, i)));
+  return r;
+}
+__device__ __forceinline__ Eight fma(const Eight& a, float b, const Eight& c) {
+  Eight r;
+#pragma unroll
+  for (int i = 0; i < kE / 2; ++i) put(r, i, __ffma2_rn(two(a, i), make_float2(b, b), two(c, i)));
+  return r;
+}
+// sum of a b over the eight
+__device__ __forceinline__ float dot(const Eight& a, const Eight& b) {
+  float2 s = __fmul2_rn(two(a, 0), two(b, 0));
+#pragma unroll
+  for (int i = 1; i < kE / 2; ++i) s = __ffma2_rn(two(a, i), two(b, i), s);
+  return s.x + s.y;
+}
+
 // Raw values as loaded (four or eight registers), so that a prefetched row costs little.
 template <typename T> struct Raw;
 template <> struct Raw<float> {
@@ -231,6 +271,13 @@ __device__ __forceinline__ Eight group_sum(const Eight& x, Team& t, const Place<
   return out;
 }
 
+__device__ __forceinline__ Eight inverse_rms(const Eight& sum, float inv, float eps) {
+  Eight r;
+#pragma unroll
+  for (int i = 0; i < kE; ++i) r.v[i] = rsqrtf(fmaf(sum.v[i], inv, eps));
+  return r;
+}
+
 // sigmoid(z) by the exponential and reciprocal instructions: e^-z is off by |z| 2^-24 of itself,
 // the sigmoid by at most s (1 - s) |z| 2^-24 < 2^-26. (expf and a division: 15 instructions more,
 // a third of a forward row.)
@@ -281,41 +328,24 @@ __global__ void __launch_bounds__(MAX_THREADS, fwd_ctas(sizeof(T) == 2, MAX_THRE
   __syncthreads();
   for (; row < a.R; row += stride) {
     const Eight hv = widen<T>(hr);
-    Eight m = params<VEC>(t.weights, pl);
-#pragma unroll
-    for (int i = 0; i < kE; ++i) m.v[i] *= hv.v[i];
+    Eight m = params<VEC>(t.weights, pl) * hv;
     if (z) {
       const Eight zv = widen<T>(zr);
+      Eight sig;
 #pragma unroll
-      for (int i = 0; i < kE; ++i) m.v[i] *= sigmoid_of(zv.v[i]);
-      if (a.act == WKV_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < kE; ++i) m.v[i] *= zv.v[i];
-      }
+      for (int i = 0; i < kE; ++i) sig.v[i] = sigmoid_of(zv.v[i]);
+      m = m * sig;
+      if (a.act == WKV_ACT_SILU) m = m * zv;
     }
     Eight xv{};
     if (x) xv = widen<T>(xr);
     if (row + stride < a.R) fetch(row + stride);
-    Eight sq;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) sq.v[i] = hv.v[i] * hv.v[i];
-    const Eight ms = group_sum<VEC, MODE>(sq, t, pl, a.group);
-#pragma unroll
-    for (int i = 0; i < kE; ++i) m.v[i] *= rsqrtf(fmaf(ms.v[i], inv_group, a.eps));
-    if (x) {
-      const Eight s = params<VEC>(t.weights + wide, pl);
-#pragma unroll
-      for (int i = 0; i < kE; ++i) m.v[i] = fmaf(s.v[i], m.v[i], xv.v[i]);
-    }
+    m = m * inverse_rms(group_sum<VEC, MODE>(hv * hv, t, pl, a.group), inv_group, a.eps);
+    if (x) m = fma(params<VEC>(t.weights + wide, pl), m, xv);
     store<T, VEC>(static_cast<T*>(a.out) + row * a.C, m, pl);
     if (a.y) {
-      float q = 0.f;
-#pragma unroll
-      for (int i = 0; i < kE; ++i) q = fmaf(m.v[i], m.v[i], q);
-      const float r2 = rsqrtf(fmaf(t.sum(q), inv_c, a.eps));
-      const Eight wn = params<VEC>(t.weights + 2 * wide, pl);
-#pragma unroll
-      for (int i = 0; i < kE; ++i) m.v[i] *= r2 * wn.v[i];
+      const float r2 = rsqrtf(fmaf(t.sum(dot(m, m)), inv_c, a.eps));
+      m = m * r2 * params<VEC>(t.weights + 2 * wide, pl);
       store<T, VEC>(static_cast<T*>(a.y) + row * a.C, m, pl);
     }
   }
@@ -366,56 +396,39 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_bwd_kernel(NormGateA
     Eight dn{};
     if (dy) dn = widen<T>(dyr);
     if (row + stride < a.R) fetch(row + stride);
-    Eight r1;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) r1.v[i] = hn.v[i] * hn.v[i];
-    r1 = group_sum<VEC, MODE>(r1, t, pl, a.group);
+    const Eight r1 =
+        inverse_rms(group_sum<VEC, MODE>(hn * hn, t, pl, a.group), inv_group, a.eps);
+    hn = hn * r1;
     const Eight w = params<VEC>(t.weights, pl);
-    float so = 0.f, sd = 0.f;
-    {
-      const Eight s = params<VEC>(t.weights + wide, pl), wn = params<VEC>(t.weights + 2 * wide, pl);
-      const Eight act = act_of();
-#pragma unroll
-      for (int i = 0; i < kE; ++i) {
-        r1.v[i] = rsqrtf(fmaf(r1.v[i], inv_group, a.eps));
-        hn.v[i] *= r1.v[i];
-        out.v[i] = fmaf(s.v[i], act.v[i] * w.v[i] * hn.v[i], out.v[i]);
-        so = fmaf(out.v[i], out.v[i], so);
-        sd = fmaf(out.v[i], dn.v[i] * wn.v[i], sd);
-      }
-    }
     if (dy) {
       const Eight wn = params<VEC>(t.weights + 2 * wide, pl);
-      const float2 both = t.sum(so, sd);
+      out = fma(params<VEC>(t.weights + wide, pl), act_of() * w * hn, out);
+      const Eight dw_n = dn * wn;
+      const float2 both = t.sum(dot(out, out), dot(out, dw_n));
       const float r2 = rsqrtf(fmaf(both.x, inv_c, a.eps));
       const float pull = r2 * r2 * both.y * inv_c;  // <dy w', out r2> r2 / C
-#pragma unroll
-      for (int i = 0; i < kE; ++i) {
-        dwn.v[i] = fmaf(dn.v[i], out.v[i] * r2, dwn.v[i]);
-        d.v[i] += r2 * (dn.v[i] * wn.v[i] - out.v[i] * pull);
-      }
+      dwn = fma(dn, out * r2, dwn);
+      d = fma(fma(out, -pull, dw_n), r2, d);
     }
     if (a.dx) store<T, VEC>(static_cast<T*>(a.dx) + row * a.C, d, pl);
-    Eight n, p, dz;
     const Eight s = params<VEC>(t.weights + wide, pl), act = act_of();
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      const float dm = d.v[i] * s.v[i], ah = act.v[i] * hn.v[i];
-      ds.v[i] = fmaf(d.v[i], ah * w.v[i], ds.v[i]);
-      dw.v[i] = fmaf(dm, ah, dw.v[i]);
-      n.v[i] = dm * w.v[i];
+    const Eight dm = d * s, ah = act * hn;
+    ds = fma(d, ah * w, ds);
+    dw = fma(dm, ah, dw);
+    Eight n = dm * w;
+    if (a.dgate) {
       // silu' = sig + z sig (1 - sig), sigmoid' = sig (1 - sig)
-      const float off = 1.f - sig.v[i];
-      dz.v[i] = n.v[i] * hn.v[i] * (silu ? fmaf(act.v[i], off, sig.v[i]) : sig.v[i] * off);
-      n.v[i] *= act.v[i];
-      p.v[i] = n.v[i] * hn.v[i];
-    }
-    if (a.dgate) store<T, VEC>(static_cast<T*>(a.dgate) + row * a.C, dz, pl);
-    p = group_sum<VEC, MODE>(p, t, pl, a.group);
+      Eight slope;
 #pragma unroll
-    for (int i = 0; i < kE; ++i)
-      n.v[i] = r1.v[i] * fmaf(-hn.v[i], p.v[i] * inv_group, n.v[i]);
-    store<T, VEC>(static_cast<T*>(a.dh) + row * a.C, n, pl);
+      for (int i = 0; i < kE; ++i) {
+        const float off = 1.f - sig.v[i];
+        slope.v[i] = silu ? ::fmaf(act.v[i], off, sig.v[i]) : sig.v[i] * off;
+      }
+      store<T, VEC>(static_cast<T*>(a.dgate) + row * a.C, n * hn * slope, pl);
+    }
+    n = n * act;
+    const Eight p = group_sum<VEC, MODE>(n * hn, t, pl, a.group) * -inv_group;
+    store<T, VEC>(static_cast<T*>(a.dh) + row * a.C, fma(hn, p, n) * r1, pl);
   }
   // the teams' sums added up in order where the weights were, a line a CTA
   float* const sums = t.weights;
