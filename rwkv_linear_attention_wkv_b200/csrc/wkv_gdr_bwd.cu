@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
   const int hk = blockIdx.x % a.Hk;
   const int64_t slot = blockIdx.x / a.Hk;
   // the sequence and chunk of this slot
-  int seq = -1, chunk = 0, len = 0;
+  int seq, chunk, len;
   int64_t t0 = 0;
   if (a.offsets == nullptr) {
     const int per = (a.T + L - 1) / L + 1;
@@ -358,19 +358,23 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     t0 = sequence(a, seq, len);
     if (chunk == per - 1) return;
   } else {
-    for (int s0 = 0; s0 < a.n_seqs && seq < 0; s0 += 32) {
-      bool mine = false;
-      if (s0 + lane < a.n_seqs) {
-        const int64_t first = sequence(a, s0 + lane, len);
-        const int64_t at = slot - gdr_chunk_base(a, s0 + lane, first);
-        mine = at >= 0 && at * L < len;
-      }
-      const unsigned who = __ballot_sync(0xffffffffu, mine);
-      if (who != 0) seq = s0 + __ffs(who) - 1;
-    }
-    if (seq < 0) return;
+    // The last sequence whose first chunk is not behind this slot, 32 candidates at a time (first
+    // chunks increase with the sequence; whatever the offsets are, the sequence found is checked).
+    int lo = 0, hi = a.n_seqs;
+    do {
+      const int step = (hi - lo + 31) / 32, s = lo + lane * step;
+      bool before = false;
+      if (s < hi) before = gdr_chunk_base(a, s, sequence(a, s, len)) <= slot;
+      const unsigned who = __ballot_sync(0xffffffffu, before);
+      if (who == 0) return;
+      lo += (31 - __clz(who)) * step;
+      hi = min(hi, lo + step);
+    } while (hi - lo > 1);
+    seq = lo;
     t0 = sequence(a, seq, len);
-    chunk = int(slot - gdr_chunk_base(a, seq, t0));
+    const int64_t at = slot - gdr_chunk_base(a, seq, t0);
+    if (at < 0 || at * L >= len) return;
+    chunk = int(at);
   }
   t0 += int64_t(chunk) * L;
   len = min(len - chunk * L, L);

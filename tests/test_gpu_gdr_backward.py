@@ -128,6 +128,20 @@ def test_backward_packed(W, N, dtype):
         assert bool((out[m][:, :2] == 7).all()) and bool((out[m][:, 166:] == 7).all())
 
 
+def test_backward_many_packed_sequences(W):
+    # more sequences than are ordered by length, most of a token or two, empty ones among them
+    gen = torch.Generator().manual_seed(26)
+    lens = torch.randint(0, 4, (1300,), generator=gen)
+    lens[[5, 700, 1299]] = torch.tensor([130, 64, 65])
+    off = [0] + torch.cumsum(lens, 0).tolist()
+    T, H, N = off[-1], 1, 64
+    x = ref.inputs((1, T), 1, H, N, FP32, 27)
+    dy = normal((1, T, H, N), 28)
+    spans = [(0, a, b) for a, b in zip(off[:-1], off[1:])]
+    got = run(W, x, 0.5, dy, None, None, off, want_dstate=False)
+    compare(got, gradients(x, 0.5, dy, None, None, spans), FP32)
+
+
 # long sequences of few heads: both walks in segments of at least 256 tokens, side by side
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("N,B,T,Hk,H", [(64, 1, 1025, 1, 2), (128, 1, 1100, 1, 1)])
