@@ -22,12 +22,11 @@ using namespace gdr;
 namespace {
 
 // leave[s] = leave[s - 1] M_s + B_s, one CTA for 64 rows of a head, 16 a warp in registers. M_s
-// goes through shared memory in three bf16 parts; the next one is fetched meanwhile.
+// goes through shared memory in three bf16 parts; the next one comes in meanwhile.
 template <int N>
 __global__ void __launch_bounds__(128) gdr_combine_kernel(GdrArgs a, GdrSegs g, bool reverse) {
   constexpr int kPitch = N + 8, kPart = N * kPitch * 2, kQuads = N / 4;
   constexpr int kPer = N * kQuads / 128;  // float4s of M a thread
-  constexpr int kAtOnce = 8;
   extern __shared__ __align__(128) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -50,31 +49,37 @@ __global__ void __launch_bounds__(128) gdr_combine_kernel(GdrArgs a, GdrSegs g, 
     return int64_t(reverse ? base + count - 1 - k : base + k) * head + int64_t(h) * N * N;
   };
   if (count <= 2) return;
+  const float4* const raw = reinterpret_cast<const float4*>(smem + 3 * kPart);
+  auto fetch = [&](int k) {
+    const float4* const M = reinterpret_cast<const float4*>(g.unit + slot_at(k));
+#pragma unroll 8
+    for (int x = 0; x < kPer; ++x) {
+      const int i = threadIdx.x + x * 128;
+      cp_async_16z(sb + 3 * kPart + i * 16, M + i, true);
+    }
+  };
+  fetch(1);
   float S[N / 8][4];
   get_state<N>(S, g.leave + slot_at(0) + r0 * N, lane);
   for (int k = 1; k < count - 1; ++k) {
-    const float4* const M = reinterpret_cast<const float4*>(g.unit + slot_at(k));
     float B[N / 8][4];
     get_state<N>(B, g.leave + slot_at(k) + r0 * N, lane);
-    __syncthreads();  // the last M has been read
-#pragma unroll 1
-    for (int x = 0; x < kPer; x += kAtOnce) {
-      float4 m[kAtOnce];
-#pragma unroll
-      for (int y = 0; y < kAtOnce; ++y) m[y] = M[threadIdx.x + (x + y) * 128];
-#pragma unroll
-      for (int y = 0; y < kAtOnce; ++y) {
-        const int i = threadIdx.x + (x + y) * 128;
-        unsigned char* d = smem + (i / kQuads * kPitch + (i % kQuads) * 4) * 2;
-        uint2 p0, p1, p2;
-        split2(m[y].x, m[y].y, p0.x, p1.x, p2.x);
-        split2(m[y].z, m[y].w, p0.y, p1.y, p2.y);
-        *reinterpret_cast<uint2*>(d) = p0;
-        *reinterpret_cast<uint2*>(d + kPart) = p1;
-        *reinterpret_cast<uint2*>(d + 2 * kPart) = p2;
-      }
+    cp_async_wait_all();
+    __syncthreads();  // M is there, the last one's parts have been read
+#pragma unroll 8
+    for (int x = 0; x < kPer; ++x) {
+      const int i = threadIdx.x + x * 128;
+      const float4 m = raw[i];
+      unsigned char* d = smem + (i / kQuads * kPitch + (i % kQuads) * 4) * 2;
+      uint2 p0, p1, p2;
+      split2(m.x, m.y, p0.x, p1.x, p2.x);
+      split2(m.z, m.w, p0.y, p1.y, p2.y);
+      *reinterpret_cast<uint2*>(d) = p0;
+      *reinterpret_cast<uint2*>(d + kPart) = p1;
+      *reinterpret_cast<uint2*>(d + 2 * kPart) = p2;
     }
     __syncthreads();
+    if (k + 1 < count - 1) fetch(k + 1);
     // B += S M, every 16 of the contraction summed on their own and added in fp32
     const uint32_t ch = sb + at_channels(lane, kPitch);
 #pragma unroll
@@ -104,7 +109,7 @@ __global__ void __launch_bounds__(128) gdr_combine_kernel(GdrArgs a, GdrSegs g, 
 
 template <int N>
 int combine(const GdrArgs& a, const GdrSegs& segs, bool reverse, cudaStream_t stream) {
-  constexpr int kSmem = 3 * N * (N + 8) * 2;
+  constexpr int kSmem = 3 * N * (N + 8) * 2 + N * N * 4;
   auto* kernel = gdr_combine_kernel<N>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
       cudaSuccess)
