@@ -7,7 +7,7 @@
 // outputs. Three times the work of one pass, over as many times the CTAs. The reverse walk is the
 // same with the segments in the other order (its M is the transpose).
 //
-// Measured, 1 x 16384 x 8 x 64 fp32 in 18 segments: 156 + 52 + 100 us against 1,480 whole. With
+// Measured, 1 x 16384 x 8 x 64 fp32 in 18 segments: 149 + 39 + 97 us against 1,480 whole. With
 // four segments a sequence (the fewest taken), whole / in segments, us: 1 x 1024 x 8 x 64 bf16 84 /
 // 77, fp32 112 / 81; 1 x 4096 x 37 x 64 bf16 251 / 186; 1 x 2048 x 16 x 128 bf16 191 / 172; 1 x 1024
 // x 18 x 128 bf16 104 / 112.
