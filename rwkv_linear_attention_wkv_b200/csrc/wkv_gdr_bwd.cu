@@ -532,13 +532,22 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     float q1[NT][4], k1[NT][4], k2[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) zero(q1[n]), zero(k1[n]), zero(k2[n]);
-    // S^T dy, S^T de; while a block of rows is at work the next is fetched
+    // S^T dy, S^T de; while a block of rows is at work the next is fetched. A sequence that starts
+    // from nothing has no gradient for its first decay, not even a rounding's.
+    bool starts = chunk > 0;
 #pragma unroll 1
     for (int r0 = 0; r0 < N; r0 += X::kRows) {
       if (r0 > 0) __syncthreads();
+      bool some = false;
+#pragma unroll
+      for (int x = 0; x < kSt; ++x)
+        some |= sr[x].x != 0.f || sr[x].y != 0.f || sr[x].z != 0.f || sr[x].w != 0.f;
       store_state(std::integral_constant<int, PA>());
       cp_async_wait_all();
-      __syncthreads();
+      if (chunk > 0)
+        __syncthreads();
+      else
+        starts |= __syncthreads_or(some) != 0;
       if (r0 + X::kRows < N)
         fetch_state(b.checkpoints + state_at, r0 + X::kRows);
       else
@@ -680,7 +689,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
         }
         x += carry;
         carry = __shfl_sync(0xffffffffu, x, 0);
-        if (t < len) b.dg[(t0 + t) * a.H + h] = base + x;
+        if (t < len) b.dg[(t0 + t) * a.H + h] = starts || t > 0 ? base + x : 0.f;
       }
     }
   }

@@ -128,6 +128,20 @@ def test_backward_packed(W, N, dtype):
         assert bool((out[m][:, :2] == 7).all()) and bool((out[m][:, 166:] == 7).all())
 
 
+@pytest.mark.parametrize("N", [64, 128])
+def test_backward_first_decay_of_nothing(W, N):
+    # without a state the first token's decay multiplies zero: its gradient is zero, and with one
+    # it is not
+    off = [0, 1, 30, 130]
+    x = ref.inputs((1, 130), 1, 2, N, BF16, 29)
+    dy = normal((1, 130, 2, N), 30, BF16)
+    for S0 in (None, 0.3 * normal((3, 2, N, N), 31)):
+        got = run(W, x, 0.5, dy, S0, None, off)
+        assert bool((got["dg"][0, off[:-1]] == 0).all()) == (S0 is None)
+        want = gradients(x, 0.5, dy, S0, None, [(0, a, b) for a, b in zip(off[:-1], off[1:])])
+        compare(got, want, BF16)
+
+
 def test_backward_many_packed_sequences(W):
     # more sequences than are ordered by length, most of a token or two, empty ones among them
     gen = torch.Generator().manual_seed(26)
