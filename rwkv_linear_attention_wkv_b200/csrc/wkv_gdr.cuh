@@ -16,8 +16,9 @@
 // Precision: a state, and what is derived from it, is fp32; as an operand it is split into three
 // bf16 parts (24 bits), so that products with bf16 inputs (one part) take 3 instructions and
 // products of two split values 6 (hi hi, hi mid, mid hi, hi lo, lo hi, mid mid: what is left out is
-// below 2^-22). fp32 inputs are split into three parts as well. What only bf16 outputs see leaves
-// out the third part (below 2^-15 of a value against their own rounding of 2^-9).
+// below 2^-22). fp32 inputs are split into three parts as well. So a bf16 result is an fp32 result
+// rounded once. (The read-outs of bf16 problems with two parts a factor, 2^-15 of a value: 754 us
+// instead of 843 at 8 x 4096 x 64 x 64, and six times as many of them on the other side of a rounding.)
 #pragma once
 
 #include <cstdint>
@@ -73,8 +74,8 @@ __device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) {
 
 // Two values as three packed bf16 parts that add up to them, 8 bits each: mid and lo by cutting
 // off, hi to the nearest, or cut off as well (CUT: two instructions less, for operands of a product
-// with exact bf16 values, where no part pair is left out; two parts are then good to 2^-15). With integer adds, masks and byte permutes: packed conversions and
-// fp32x2 arithmetic take as many instructions, but wait for one another and for the matrix
+// with exact bf16 values, where no part pair is left out; two parts are then good to 2^-15). With
+// integer adds, masks and byte permutes: packed conversions and fp32x2 arithmetic take as many instructions, but wait for one another and for the matrix
 // instructions (16 such splits beside 16 matrix instructions, cycles a scheduler: 435 with
 // conversions, 298 this way; 129 for the matrix instructions alone).
 template <bool CUT = false>
@@ -110,12 +111,10 @@ __device__ __forceinline__ void scale_add(float (&s)[4], float c, const float (&
 }
 
 // The part pairs of a product, largest first: P operand parts of b (1: exact bf16, 3: split).
-// FULL leaves out none of the six (three with P = 1) that fp32 accuracy takes; without it the
-// pairs below 2^-15 go.
 // Each pair is two digits, a's part and b's, in the packed lists.
-template <int P, bool FULL>
+template <int P>
 struct Pairs {
-  static constexpr int n = P == 1 ? (FULL ? 3 : 2) : (FULL ? 6 : 3);
+  static constexpr int n = P == 1 ? 3 : 6;
   static constexpr uint32_t as = P == 1 ? 0x210u : 0x120100u;
   static constexpr uint32_t bs = P == 1 ? 0x000u : 0x102010u;
   __device__ static constexpr int a(int i) { return int(as >> (4 * i)) & 15; }
@@ -125,10 +124,10 @@ struct Pairs {
 // main += hi hi, corr += the other pairs, over two column tiles whose b parts are b[p][0..3]
 // (tile 0: registers 0, 1; tile 1: 2, 3). Separate sums, so that the small products are not
 // rounded into the large sum one by one.
-template <int P, bool FULL>
+template <int P>
 __device__ __forceinline__ void mma_pairs(float (&main)[2][4], float (&corr)[2][4],
                                           const uint32_t (&a)[3][4], const uint32_t (&b)[P][4]) {
-  using X = Pairs<P, FULL>;
+  using X = Pairs<P>;
 #pragma unroll
   for (int i = 0; i < X::n; ++i)
 #pragma unroll
@@ -137,10 +136,10 @@ __device__ __forceinline__ void mma_pairs(float (&main)[2][4], float (&corr)[2][
 }
 
 // One sum, the small products first.
-template <int P, bool FULL>
+template <int P>
 __device__ __forceinline__ void mma_up(float (&c)[2][4], const uint32_t (&a)[3][4],
                                        const uint32_t (&b)[P][4]) {
-  using X = Pairs<P, FULL>;
+  using X = Pairs<P>;
 #pragma unroll
   for (int i = X::n - 1; i >= 0; --i)
 #pragma unroll
@@ -488,7 +487,7 @@ __device__ __forceinline__ void group_product(float (&c)[2][4], Tile tile, int A
 #pragma unroll
       for (int n = 0; n < 2; ++n) mma(c[n], a[0], b[0][2 * n], b[0][2 * n + 1]);
     } else {
-      mma_pairs<P, true>(c, corr, a, b);
+      mma_pairs<P>(c, corr, a, b);
     }
   }
   if (P > 1) {
@@ -500,8 +499,7 @@ __device__ __forceinline__ void group_product(float (&c)[2][4], Tile tile, int A
 }
 
 // Two pairs of adjacent accumulator tiles (rows: the product's columns) as the b operand of a
-// 16 x 16 product, PARTS parts of a uint4 a lane.
-template <int PARTS>
+// 16 x 16 product, three parts of a uint4 a lane.
 __device__ __forceinline__ void put_fragment(uint4 (*to)[32], const float2& t00, const float2& t01,
                                              const float2& t10, const float2& t11, int lane) {
   uint4 f[3];
@@ -510,7 +508,7 @@ __device__ __forceinline__ void put_fragment(uint4 (*to)[32], const float2& t00,
   split2(t10.x, t10.y, f[0].z, f[1].z, f[2].z);
   split2(t11.x, t11.y, f[0].w, f[1].w, f[2].w);
 #pragma unroll
-  for (int p = 0; p < PARTS; ++p) to[p][lane] = f[p];
+  for (int p = 0; p < 3; ++p) to[p][lane] = f[p];
 }
 
 // A warp's 16 channels x 16 tokens (accumulator tiles) to rows of tokens in global memory:
@@ -777,7 +775,7 @@ __device__ __forceinline__ void produce(const GdrArgs& a, const void* vals, cons
           return REVERSE ? make_float2(L[j * kLP + i], L[(j + 1) * kLP + i])
                          : *reinterpret_cast<const float2*>(L + i * kLP + j);
         };
-        put_fragment<3>(m.inv, pair(g4, 2 * t4), pair(g4, 8 + 2 * t4), pair(g4 + 8, 2 * t4),
+        put_fragment(m.inv, pair(g4, 2 * t4), pair(g4, 8 + 2 * t4), pair(g4 + 8, 2 * t4),
                         pair(g4 + 8, 8 + 2 * t4), lane);
         __syncwarp();
       }
@@ -802,8 +800,7 @@ __device__ __forceinline__ void produce(const GdrArgs& a, const void* vals, cons
             }
           }
         auto two = [](const float(&t)[4], int j) { return make_float2(t[j], t[j + 1]); };
-        put_fragment<!REVERSE && X::kBf16 ? 2 : 3>(m.read, two(qk[0], 0), two(qk[1], 0),
-                                                   two(qk[0], 2), two(qk[1], 2), lane);
+        put_fragment(m.read, two(qk[0], 0), two(qk[1], 0), two(qk[0], 2), two(qk[1], 2), lane);
         const Decay last = shfl(cs, 15);
         if (lane < kG) {
           const float d = ex2(cs.hi + cs.lo), to_end = decay_between(last, cs);

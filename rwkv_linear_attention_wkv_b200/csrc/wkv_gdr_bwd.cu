@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
 #pragma unroll
         for (int p = 0; p < P; ++p) ldsm4(kb[p], tile(i, 0, p) + to + c * 2);
         split_tiles<X::kBf16>(S[c / 8], S[c / 8 + 1], parts);
-        mma_pairs<P, true>(xm, xc, parts, kb);
+        mma_pairs<P>(xm, xc, parts, kb);
       }
       // R^T
       float vv[2][4], r[2][4];
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
         mma_exact_a(r, raw, fb);
       } else {
         split_tiles(vv[0], vv[1], ap);
-        mma_up<3, true>(r, ap, fb);
+        mma_up<3>(r, ap, fb);
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
       float ec[2][4];
       zero(ec[0]);
       zero(ec[1]);
-      mma_up<3, true>(ec, ap, fb);
+      mma_up<3>(ec, ap, fb);
       float de[2][4], w1[2][4], w2[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
         float d[2][4];
         zero(d[0]);
         zero(d[1]);
-        mma_up<P, true>(d, ap, qb);
-        mma_up<P, true>(d, bp, kb);
+        mma_up<P>(d, ap, qb);
+        mma_up<P>(d, bp, kb);
 #pragma unroll
         for (int n = 0; n < 2; ++n) scale_add(S[c / 8 + n], end, d[n]);
       }

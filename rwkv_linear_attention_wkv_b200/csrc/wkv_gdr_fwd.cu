@@ -9,10 +9,10 @@
 // registers, and the products run transposed (channels x tokens): S_0 K^T and S_0 Q^T take the
 // state as operand a in place, e^T and the weighted e^T become operands as they come out.
 //
-// Bound by issue slots: a group of a head takes 2,900 warp instructions, 344 of them matrix
+// Bound by issue slots: a group of a head takes 2,960 warp instructions, 400 of them matrix
 // instructions of 8 cycles that hold the issue port for about 4.5, so that the matrix time adds to
-// the rest instead of hiding behind it (8 x 4096 x 64 x 64 bf16: 754 us, matrix pipe half busy,
-// 0.22 of HBM). More warps do not help (three CTAs of 96 registers: 844 us), fewer instructions do.
+// the rest instead of hiding behind it (8 x 4096 x 64 x 64 bf16: 843 us, 0.20 of HBM). More warps do
+// not help (three CTAs of 96 registers took 8 % longer), fewer instructions do.
 // Few heads are bound by a group's chain of products, 0.9 us (bf16, 64): see wkv_gdr_seg.cu.
 //
 // A CTA has 64 value channels of one head of one sequence (or of a segment of it): two or four
@@ -97,10 +97,10 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
           if (!SUMMARY) ldsm4(qb[p], tile(i, 1, p) + to + c * 2);
         }
         split_tiles<X::kBf16>(S[c / 8], S[c / 8 + 1], parts);
-        mma_pairs<P, true>(xm, xc, parts, kb);
+        mma_pairs<P>(xm, xc, parts, kb);
         // (one sum where only a bf16 y sees it: 8 registers less)
-        if constexpr (!SUMMARY && X::kBf16) mma_up<P, false>(om, parts, qb);
-        if constexpr (!SUMMARY && !X::kBf16) mma_pairs<P, true>(om, oc, parts, qb);
+        if constexpr (!SUMMARY && X::kBf16) mma_up<P>(om, parts, qb);
+        if constexpr (!SUMMARY && !X::kBf16) mma_pairs<P>(om, oc, parts, qb);
       }
       // e: V^T - C_i X as accumulator, plus its product with (I + A)^-1 - I
       float e[2][4], ec[2][4];
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
       split_tiles(e[0], e[1], ep);
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(fb[p]) = m.inv[p][lane];
-      mma_up<3, true>(ec, ep, fb);
+      mma_up<3>(ec, ep, fb);
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -130,12 +130,11 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
       // y: scale C_i S_0 Q^T plus the read matrix times e
       split_tiles(e[0], e[1], ep);
 #pragma unroll
-      for (int p = 0; p < (X::kBf16 ? 2 : 3); ++p)
-        *reinterpret_cast<uint4*>(fb[p]) = m.read[p][lane];
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(fb[p]) = m.read[p][lane];
       float o[2][4];
       zero(o[0]);
       zero(o[1]);
-      if (!SUMMARY) mma_up<3, !X::kBf16>(o, ep, fb);
+      if (!SUMMARY) mma_up<3>(o, ep, fb);
       float w[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
         float d[2][4];
         zero(d[0]);
         zero(d[1]);
-        mma_up<P, true>(d, wp, kb);
+        mma_up<P>(d, wp, kb);
 #pragma unroll
         for (int n = 0; n < 2; ++n) scale_add(S[c / 8 + n], end, d[n]);
       }

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(128) gdr_combine_kernel(GdrArgs a, GdrSegs g, 
         float d[2][4];
         zero(d[0]);
         zero(d[1]);
-        mma_up<3, true>(d, sp, mb);
+        mma_up<3>(d, sp, mb);
 #pragma unroll
         for (int x = 0; x < 4; ++x) B[n][x] += d[0][x], B[n + 1][x] += d[1][x];
       }
