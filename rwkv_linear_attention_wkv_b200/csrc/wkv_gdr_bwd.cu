@@ -19,16 +19,14 @@
 //    (c_i enters with a plus where token i reads: q_i . dq_i, and de_i . (e_i - v_i) in the error;
 //    and with a minus where it writes: u_i . du_i = e_i . de_i.)
 //
-// Rounding: the chain keeps the full three-part products everywhere (its results feed fp32
-// gradients of states), and so does the second kernel for fp32 problems and in whatever leads to
-// dg. What only the bf16 dk sees takes two parts (2^-15 a factor).
+// Rounding: both kernels keep the full three-part products everywhere, so that a bf16 gradient is
+// an fp32 gradient rounded once. What only the bf16 dk sees is added up by the matrix instructions
+// alone (see product()).
 //
 // Measured, 16 x 1024 x 12 x 64 bf16: chain 122 us, second kernel 196 us. The chain is bound like
 // the forward (wkv_gdr_fwd.cu). The second kernel issues a third of the time and has its matrix
 // pipe busy a quarter: 16 warps an SM wait for each other's tiles (barriers) and for e, du and
 // states, 2 KB a token and head, which HBM delivers in 55 us.
-#include <type_traits>
-
 #include "wkv_gdr.cuh"
 
 namespace wkv {
@@ -208,8 +206,7 @@ struct Chunk {
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int kLen = gdr_chunk(kBf16, N);    // tokens
   static constexpr int kIn = kBf16 ? 1 : 3;           // parts of q, k, dy
-  static constexpr int kParts = kBf16 ? 2 : 3;        // parts that dk needs of u, de, states, P, Z
-  static constexpr int kAll = 3;                      // parts that dg needs of u, S, P
+  static constexpr int kParts = 3;                    // parts of u, de, states, P, Z
   // Columns of a warp: such that an SM holds 16 warps (two CTAs of 8 for bf16 heads of 64, else one
   // of 16) at 128 registers.
   static constexpr int kCols = kBf16 ? 32 : 16;
@@ -227,9 +224,9 @@ struct Chunk {
   static constexpr int kOffQ = kOffK + kIn * kTile;
   static constexpr int kOffDy = kOffQ + kIn * kTile;
   static constexpr int kOffU = kOffDy + kIn * kTile;
-  static constexpr int kOffDe = kOffU + kAll * kTile;   // later Z
+  static constexpr int kOffDe = kOffU + kParts * kTile;   // later Z
   static constexpr int kOffS = kOffDe + kParts * kTile;  // 64 rows of a state; later P
-  static constexpr int kOffF = kOffS + kAll * kState;    // floats
+  static constexpr int kOffF = kOffS + kParts * kState;    // floats
   static_assert(kPTile <= kTile && kPTile <= kState, "Z and P fit where de and the states were");
   struct Floats {
     Decay c[kLen];
@@ -254,14 +251,14 @@ __device__ __forceinline__ float4 widen(const uint2& r) {
   return make_float4(lo.x, lo.y, hi.x, hi.y);
 }
 
-// One value as PARTS bf16 parts, four at a time, PART bytes apart.
-template <int PARTS, int PART, bool CUT>
+// One value as three bf16 parts, four at a time, PART bytes apart.
+template <int PART>
 __device__ __forceinline__ void put_parts(unsigned char* d, float4 x) {
   uint2 p[3];
-  split2<CUT>(x.x, x.y, p[0].x, p[1].x, p[2].x);
-  split2<CUT>(x.z, x.w, p[0].y, p[1].y, p[2].y);
+  split2(x.x, x.y, p[0].x, p[1].x, p[2].x);
+  split2(x.z, x.w, p[0].y, p[1].y, p[2].y);
 #pragma unroll
-  for (int i = 0; i < PARTS; ++i) *reinterpret_cast<uint2*>(d + i * PART) = p[i];
+  for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(d + i * PART) = p[i];
 }
 
 // Products of operands of PA and PB parts: what a factor's parts leave out, the pairs do too.
@@ -336,7 +333,7 @@ template <typename T, int N, bool SHARED>
 __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     gdr_chunk_kernel(GdrBwdArgs b) {
   using X = Chunk<T, N>;
-  constexpr int PI = X::kIn, PP = X::kParts, PA = X::kAll, NT = X::kCols / 8, L = X::kLen;
+  constexpr int PI = X::kIn, PP = X::kParts, NT = X::kCols / 8, L = X::kLen;
   constexpr bool kExact = !X::kBf16;  // of what only dk sees
   extern __shared__ __align__(128) unsigned char smem[];
   typename X::Floats& F = *reinterpret_cast<typename X::Floats*>(smem + X::kOffF);
@@ -395,7 +392,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
         const int t = i / kQuads, c = (i % kQuads) * 4;
         float4 x = *reinterpret_cast<const float4*>(src + min(t, len - 1) * row + c);
         if (t >= len) x = make_float4(0.f, 0.f, 0.f, 0.f);
-        put_parts<3, X::kTile, false>(smem + off + (t * X::kPitch + c) * 2, x);
+        put_parts<X::kTile>(smem + off + (t * X::kPitch + c) * 2, x);
       }
     }
   };
@@ -472,12 +469,12 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
       for (int x = 0; x < kSt; ++x)
         sr[x] = reinterpret_cast<const float4*>(src + r0 * N)[threadIdx.x + x * X::kThreads];
     };
-    auto store_state = [&](auto parts) {
+    auto store_state = [&] {
 #pragma unroll
       for (int x = 0; x < kSt; ++x) {
         const int i = threadIdx.x + x * X::kThreads;
-        put_parts<decltype(parts)::value, X::kState, X::kBf16>(
-            smem + X::kOffS + (i / kQuads * X::kPitch + (i % kQuads) * 4) * 2, sr[x]);
+        put_parts<X::kState>(smem + X::kOffS + (i / kQuads * X::kPitch + (i % kQuads) * 4) * 2,
+                             sr[x]);
       }
     };
     fetch_state(b.checkpoints + state_at, 0);
@@ -522,10 +519,10 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
         if (in) b.dbeta[(t0 + t) * a.H + h] = s;
       }
       const int to = (t * X::kPitch + c) * 2;
-      put_parts<PA, X::kTile, X::kBf16>(smem + X::kOffU + to,
-                              make_float4(be * e.x, be * e.y, be * e.z, be * e.w));
-      put_parts<PP, X::kTile, X::kBf16>(smem + X::kOffDe + to,
-                              make_float4(be * d.x, be * d.y, be * d.z, be * d.w));
+      put_parts<X::kTile>(smem + X::kOffU + to,
+                          make_float4(be * e.x, be * e.y, be * e.z, be * e.w));
+      put_parts<X::kTile>(smem + X::kOffDe + to,
+                          make_float4(be * d.x, be * d.y, be * d.z, be * d.w));
     }
     const uint32_t rows = at_rows(lane, X::kPitch) + uint32_t(strip * 16 * X::kPitch) * 2u;
     const uint32_t cols = at_channels(lane, X::kPitch) + uint32_t(slice * X::kCols) * 2u;
@@ -542,7 +539,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
 #pragma unroll
       for (int x = 0; x < kSt; ++x)
         some |= sr[x].x != 0.f || sr[x].y != 0.f || sr[x].z != 0.f || sr[x].w != 0.f;
-      store_state(std::integral_constant<int, PA>());
+      store_state();
       cp_async_wait_all();
       if (chunk > 0)
         __syncthreads();
@@ -552,7 +549,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
         fetch_state(b.checkpoints + state_at, r0 + X::kRows);
       else
         fetch_state(b.dstates + state_at, 0);
-      product<PI, PA, NT, false, true, true>(q1, 0, X::kRows, sb + X::kOffDy + rows + r0 * 2,
+      product<PI, PP, NT, false, true, true>(q1, 0, X::kRows, sb + X::kOffDy + rows + r0 * 2,
                                              X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
                                              X::kPitch);
       product<PP, PP, NT, false, true, kExact>(k1, 0, X::kRows, sb + X::kOffDe + rows + r0 * 2,
@@ -570,7 +567,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
         nr[x] = reinterpret_cast<const float4*>(b.checkpoints + next_at +
                                                 r0 * N)[threadIdx.x + x * X::kThreads];
       __syncthreads();
-      store_state(std::integral_constant<int, PP>());
+      store_state();
 #pragma unroll
       for (int x = 0; x < kSt; ++x)
         inner = fmaf(sr[x].x, nr[x].x, fmaf(sr[x].y, nr[x].y,
@@ -611,7 +608,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     if (tiles > 0) {
       const uint32_t us =
           sb + X::kOffU + at_tokens(lane, X::kPitch) + uint32_t(j0 * X::kPitch) * 2u;
-      product<PI, PA, NW, false, false, true>(pw, 0, N, sb + X::kOffDy + rows, X::kTile, X::kPitch,
+      product<PI, PP, NW, false, false, true>(pw, 0, N, sb + X::kOffDy + rows, X::kTile, X::kPitch,
                                               us, X::kTile, X::kPitch, tiles);
       product<PP, PP, NW, false, false, kExact>(zw, 0, N, sb + X::kOffDe + rows, X::kTile,
                                                 X::kPitch, us, X::kTile, X::kPitch, tiles);
@@ -628,11 +625,11 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
         const float d1 = i >= j + 1 ? decay_between(ci, F.c[j + 1]) : 0.f;
         uint32_t p[3];
         const int to = (i * X::kPPitch + j) * 2;
-        split2<X::kBf16>(a.scale * d0 * pw[n][2 * z], a.scale * d1 * pw[n][2 * z + 1], p[0], p[1], p[2]);
+        split2(a.scale * d0 * pw[n][2 * z], a.scale * d1 * pw[n][2 * z + 1], p[0], p[1], p[2]);
 #pragma unroll
-        for (int x = 0; x < PA; ++x)
+        for (int x = 0; x < PP; ++x)
           *reinterpret_cast<uint32_t*>(smem + X::kOffS + x * X::kPTile + to) = p[x];
-        split2<X::kBf16>(i > j ? d0 * zw[n][2 * z] : 0.f, i > j + 1 ? d1 * zw[n][2 * z + 1] : 0.f, p[0], p[1],
+        split2(i > j ? d0 * zw[n][2 * z] : 0.f, i > j + 1 ? d1 * zw[n][2 * z + 1] : 0.f, p[0], p[1],
                p[2]);
 #pragma unroll
         for (int x = 0; x < PP; ++x)
@@ -643,7 +640,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     const uint32_t prow = at_rows(lane, X::kPPitch) + uint32_t(strip * 16 * X::kPPitch) * 2u;
     const uint32_t pcol = at_tokens(lane, X::kPPitch) + uint32_t(strip * 16) * 2u;
     const int below = strip * 16, upto = strip * 16 + 16;
-    product<PA, PI, NT, false, true, true>(q1, 0, upto, sb + X::kOffS + prow, X::kPTile, X::kPPitch,
+    product<PP, PI, NT, false, true, true>(q1, 0, upto, sb + X::kOffS + prow, X::kPTile, X::kPPitch,
                                            sb + X::kOffK + cols, X::kTile, X::kPitch);
     product<PP, PI, NT, true, true, kExact>(k2, below, L, sb + X::kOffS + pcol, X::kPTile,
                                             X::kPPitch, sb + X::kOffQ + cols, X::kTile, X::kPitch);

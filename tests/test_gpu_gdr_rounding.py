@@ -43,3 +43,18 @@ def test_read_outs(W, N, T, Hk, H):
     y, _ = W.wkv_gdr_forward(*[t.cuda() for t in x], state=S0.cuda(), scale=N ** -0.5)
     want, _ = ref.rule(*[t[0] for t in x], N ** -0.5, S0[0])
     assert_rounded(y[0], want, 2.0 ** -18, "y")
+
+
+@pytest.mark.parametrize("N,T,Hk,H", [(64, 400, 4, 4), (64, 300, 2, 4), (128, 300, 2, 2),
+                                      (128, 200, 1, 2)])
+def test_gradients(W, N, T, Hk, H):
+    gen = torch.Generator().manual_seed(83)
+    x = ref.inputs((1, T), Hk, H, N, BF16, 84)
+    S0, dS = (0.3 * torch.randn(1, H, N, N, generator=gen) for _ in range(2))
+    dy = torch.randn(1, T, H, N, generator=gen).to(BF16)
+    c = [t.cuda() for t in x]
+    y, _, ws = W.wkv_gdr_forward_checkpointed(*c, state=S0.cuda(), scale=N ** -0.5)
+    got = W.wkv_gdr_backward(*c, dy.cuda(), ws, grad_state=dS.cuda(), scale=N ** -0.5)
+    want = ref.rule_gradients(*[t[0] for t in x], N ** -0.5, dy[0], S0[0], dS[0])
+    for n in ("dq", "dv", "dk"):
+        assert_rounded(got[n][0], want[n], 2.0 ** -17, n)
