@@ -369,8 +369,8 @@ WKV_API int wkv_gdr_forward(const wkv_gdr_problem* p, const void* q, const void*
 /*
  * The pair for training. The forward also keeps, in `checkpoints` (device, 16-byte aligned,
  * wkv_gdr_checkpoint_bytes(p) bytes: 0 where there is nothing to keep), every token's e_t in
- * fp32, the state entering every 64 tokens of a sequence (32 for fp32 heads of 128) and the one
- * leaving it. The backward gives the gradients of sum(dy y) + sum(ds1 s1) from the same inputs
+ * fp32 and the state entering every 64 tokens of a sequence (32 for fp32 heads of 128), and has
+ * room for one state more a sequence. The backward gives the gradients of sum(dy y) + sum(ds1 s1) from the same inputs
  * and those checkpoints, which it only reads: dq, dk as q; dv as v; dg, dbeta
  * fp32 (B, T, H); ds0 as the states. ds1 NULL = zero; ds0 NULL = not wanted, and may be ds1. dq
  * and dk are summed over the value heads that share them; every sum has a fixed order. No

@@ -15,9 +15,13 @@
 //      dq = scale C S^T dy + P K
 //      dk = [exp(c_L - c) dD^T u + P^T Q - Z^T K] + [-C S^T de - Z K]
 //      dbeta_j = du_j . e_j
-//      dg_t = <dD, S_L> + sum_{i >= t} q_i . dq_i - v_i . dv_i,   S_L the state that leaves.
-//    (c_i enters with a plus where token i reads: q_i . dq_i, and de_i . (e_i - v_i) in the error;
-//    and with a minus where it writes: u_i . du_i = e_i . de_i.)
+//      dg_t = sum_{i >= t} R_i + sum_{j < t} W_j + sum_{i >= t > j} X_ij + C_L <dD, S>
+//      R_i = q_i . scale C_i S^T dy_i - k_i . C_i S^T de_i,   W_j = k_j . exp(c_L - c_j) dD^T u_j
+//      X_ij = P_ij (q_i . k_j) - Z_ij (k_i . k_j)
+//    These are the terms whose decays pass t: read from the state or written to it on this side of
+//    t or that, or both. Each carries e^{g_t} itself. (The gradient of every running sum c_i, added
+//    up from the end, is shorter, but there the terms on one side of t have to cancel: nothing but
+//    rounding was left of dg_t at g_t = -16, and something at -inf.)
 //
 // Rounding: both kernels keep the full three-part products everywhere, so that a bf16 gradient is
 // an fp32 gradient rounded once. What only the bf16 dk sees is added up by the matrix instructions
@@ -228,28 +232,22 @@ struct Chunk {
   static constexpr int kOffS = kOffDe + kParts * kTile;  // 64 rows of a state; later P
   static constexpr int kOffF = kOffS + kParts * kState;    // floats
   static_assert(kPTile <= kTile && kPTile <= kState, "Z and P fit where de and the states were");
+  static constexpr int kShares = kSlices < kLen / 16 ? kSlices : kLen / 16;  // of P's columns
+  static constexpr int kShare = kLen / kShares;
   struct Floats {
     Decay c[kLen];
     float beta[kLen];
-    float to_end[kLen];      // exp(c_L - c_j)
-    float since[kLen];       // C_i
-    float written[kLen];     // v . dv
-    float read[kSlices][kLen];  // q . dq by slice of the columns
-    float inner[kWarps];     // <dD, S_L> by warp
+    float to_end[kLen];           // exp(c_L - c_j)
+    float since[kLen];            // C_i
+    float read[kSlices][kLen];    // R_i by slice of the columns
+    float wrote[kSlices][kLen];   // W_j, the same
+    float across[kLen / 16][kLen];  // sum of X_ij over i >= t of a strip and j < t of t's share
+    float rows[kShares][kLen];    // sum of X_ij over a share's j
+    float inner[kWarps];          // <dD, S> by warp
   };
   static constexpr int kSmem = kOffF + int(sizeof(Floats));
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "the CTAs' shared memory fits an SM");
 };
-
-// Four values as they are in memory.
-template <typename T> struct Raw4;
-template <> struct Raw4<float> { typedef float4 Type; };
-template <> struct Raw4<__nv_bfloat16> { typedef uint2 Type; };
-template <typename T> using Four = typename Raw4<T>::Type;
-__device__ __forceinline__ float4 widen(const float4& x) { return x; }
-__device__ __forceinline__ float4 widen(const uint2& r) {
-  const float2 lo = unpack(r.x), hi = unpack(r.y);
-  return make_float4(lo.x, lo.y, hi.x, hi.y);
-}
 
 // One value as three bf16 parts, four at a time, PART bytes apart.
 template <int PART>
@@ -399,7 +397,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
   load_input(static_cast<const T*>(a.k) + t0 * qk_row + int64_t(hk) * N, qk_row, X::kOffK);
   load_input(static_cast<const T*>(a.q) + t0 * qk_row + int64_t(hk) * N, qk_row, X::kOffQ);
 
-  // sum over this thread's columns of x times an input's rows, for its two tokens, left in F.dots
+  // sum over a warp's columns of x times an input's rows, for the two tokens of a thread
   auto dot_rows = [&](const float(&x)[NT][4], int off, float(&out)[2]) {
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
@@ -452,7 +450,6 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     // what the head needs first, on its way before anything is waited for
     constexpr int kTok = L * kQuads / X::kThreads, kSt = X::kRows * kQuads / X::kThreads;
     float4 er[kTok], dr[kTok], sr[kSt];
-    Four<T> vr[kTok];
     // (rows past the end read the last one: a branch would put the loads one after the other)
 #pragma unroll
     for (int x = 0; x < kTok; ++x) {
@@ -461,7 +458,6 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
           (t0 + min(i / kQuads, len - 1)) * v_row + int64_t(h) * N + (i % kQuads) * 4;
       er[x] = *reinterpret_cast<const float4*>(b.e + at);
       dr[x] = *reinterpret_cast<const float4*>(b.du + at);
-      vr[x] = *reinterpret_cast<const Four<T>*>(static_cast<const T*>(a.v) + at);
     }
     // 64 rows of a state, from global memory and into parts
     auto fetch_state = [&](const float* src, int r0) {
@@ -499,25 +495,18 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
       F.beta[t] = t < len ? a.beta[(t0 + t) * a.H + h] : 0.f;
     }
     __syncthreads();
-    // u, de, dbeta, v . dv: a token's row lies in kQuads adjacent lanes
+    // u, de, dbeta: a token's row lies in kQuads adjacent lanes
 #pragma unroll
     for (int x = 0; x < kTok; ++x) {
       const int i = threadIdx.x + x * X::kThreads, t = i / kQuads, c = (i % kQuads) * 4;
       const bool in = t < len;
       const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 e = in ? er[x] : zero4, d = in ? dr[x] : zero4, v = in ? widen(vr[x]) : zero4;
+      const float4 e = in ? er[x] : zero4, d = in ? dr[x] : zero4;
       const float be = F.beta[t];
       float s = fmaf(e.x, d.x, fmaf(e.y, d.y, fmaf(e.z, d.z, e.w * d.w)));
-      float w = fmaf(v.x, d.x, fmaf(v.y, d.y, fmaf(v.z, d.z, v.w * d.w)));
 #pragma unroll
-      for (int m = kQuads / 2; m >= 1; m >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, m);
-        w += __shfl_xor_sync(0xffffffffu, w, m);
-      }
-      if (c == 0) {
-        F.written[t] = be * w;
-        if (in) b.dbeta[(t0 + t) * a.H + h] = s;
-      }
+      for (int m = kQuads / 2; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+      if (c == 0 && in) b.dbeta[(t0 + t) * a.H + h] = s;
       const int to = (t * X::kPitch + c) * 2;
       put_parts<X::kTile>(smem + X::kOffU + to,
                           make_float4(be * e.x, be * e.y, be * e.z, be * e.w));
@@ -529,22 +518,13 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     float q1[NT][4], k1[NT][4], k2[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) zero(q1[n]), zero(k1[n]), zero(k2[n]);
-    // S^T dy, S^T de; while a block of rows is at work the next is fetched. A sequence that starts
-    // from nothing has no gradient for its first decay, not even a rounding's.
-    bool starts = chunk > 0;
+    // S^T dy, S^T de; while a block of rows is at work the next is fetched
 #pragma unroll 1
     for (int r0 = 0; r0 < N; r0 += X::kRows) {
       if (r0 > 0) __syncthreads();
-      bool some = false;
-#pragma unroll
-      for (int x = 0; x < kSt; ++x)
-        some |= sr[x].x != 0.f || sr[x].y != 0.f || sr[x].z != 0.f || sr[x].w != 0.f;
       store_state();
       cp_async_wait_all();
-      if (chunk > 0)
-        __syncthreads();
-      else
-        starts |= __syncthreads_or(some) != 0;
+      __syncthreads();
       if (r0 + X::kRows < N)
         fetch_state(b.checkpoints + state_at, r0 + X::kRows);
       else
@@ -552,19 +532,18 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
       product<PI, PP, NT, false, true, true>(q1, 0, X::kRows, sb + X::kOffDy + rows + r0 * 2,
                                              X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
                                              X::kPitch);
-      product<PP, PP, NT, false, true, kExact>(k1, 0, X::kRows, sb + X::kOffDe + rows + r0 * 2,
+      product<PP, PP, NT, false, true, true>(k1, 0, X::kRows, sb + X::kOffDe + rows + r0 * 2,
                                                X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
                                                X::kPitch);
     }
-    // dD^T u, and <dD, S_L>
+    // dD^T u, and <dD, S>
     float inner = 0.f;
-    const int64_t next_at = state_at + int64_t(a.H) * N * N;
 #pragma unroll 1
     for (int r0 = 0; r0 < N; r0 += X::kRows) {
       float4 nr[kSt];
 #pragma unroll
       for (int x = 0; x < kSt; ++x)
-        nr[x] = reinterpret_cast<const float4*>(b.checkpoints + next_at +
+        nr[x] = reinterpret_cast<const float4*>(b.checkpoints + state_at +
                                                 r0 * N)[threadIdx.x + x * X::kThreads];
       __syncthreads();
       store_state();
@@ -574,7 +553,7 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
                      fmaf(sr[x].z, nr[x].z, fmaf(sr[x].w, nr[x].w, inner))));
       __syncthreads();
       if (r0 + X::kRows < N) fetch_state(b.dstates + state_at, r0 + X::kRows);
-      product<PP, PP, NT, false, true, kExact>(k2, 0, X::kRows, sb + X::kOffU + rows + r0 * 2,
+      product<PP, PP, NT, false, true, true>(k2, 0, X::kRows, sb + X::kOffU + rows + r0 * 2,
                                                X::kTile, X::kPitch, sb + X::kOffS + cols, X::kState,
                                                X::kPitch);
     }
@@ -594,15 +573,26 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
           k1[n][x] *= since[x >> 1];
           k2[n][x] *= to_end[x >> 1];
         }
+      // what dg needs of them, before the chunk's own tokens join
+      float rq[2], rk[2], wk[2];
+      dot_rows(q1, X::kOffQ, rq);
+      dot_rows(k1, X::kOffK, rk);
+      dot_rows(k2, X::kOffK, wk);
+      if (t4 == 0) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          F.read[slice][t + z * 8] = rq[z] - rk[z];
+          F.wrote[slice][t + z * 8] = wk[z];
+        }
+      }
     }
     // P and Z: this warp's tokens i, its share of the columns j
-    constexpr int kShares = X::kSlices < L / 16 ? X::kSlices : L / 16;
-    constexpr int NW = L / kShares / 8;  // column tiles of a warp
-    const bool shares = slice < kShares;
+    constexpr int NW = X::kShare / 8;  // column tiles of a warp
+    const bool shares = slice < X::kShares;
     float pw[NW][4], zw[NW][4];
 #pragma unroll
     for (int n = 0; n < NW; ++n) zero(pw[n]), zero(zw[n]);
-    const int j0 = slice * (L / kShares);
+    const int j0 = slice * X::kShare;
     // (16 x 16 blocks above the diagonal are neither made nor read)
     const int tiles = shares ? (strip + 1) * 2 - j0 / 8 : 0;
     if (tiles > 0) {
@@ -610,8 +600,64 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
           sb + X::kOffU + at_tokens(lane, X::kPitch) + uint32_t(j0 * X::kPitch) * 2u;
       product<PI, PP, NW, false, false, true>(pw, 0, N, sb + X::kOffDy + rows, X::kTile, X::kPitch,
                                               us, X::kTile, X::kPitch, tiles);
-      product<PP, PP, NW, false, false, kExact>(zw, 0, N, sb + X::kOffDe + rows, X::kTile,
-                                                X::kPitch, us, X::kTile, X::kPitch, tiles);
+      product<PP, PP, NW, false, false, true>(zw, 0, N, sb + X::kOffDe + rows, X::kTile,
+                                              X::kPitch, us, X::kTile, X::kPitch, tiles);
+      // P and Z by elements, and X: sums over the columns before t, added up over the rows from t
+      const uint32_t ks =
+          sb + X::kOffK + at_tokens(lane, X::kPitch) + uint32_t(j0 * X::kPitch) * 2u;
+      float before[2] = {0.f, 0.f};  // this row's sums over the columns so far
+#pragma unroll
+      for (int n = 0; n < NW; n += 2) {
+        if (n >= tiles) continue;
+        float qk[2][4], kk[2][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) zero(qk[m]), zero(kk[m]);
+        const uint32_t kn = ks + uint32_t(n * 8 * X::kPitch) * 2u;
+        product<PI, PI, 2, false, false, true>(qk, 0, N, sb + X::kOffQ + rows, X::kTile, X::kPitch,
+                                               kn, X::kTile, X::kPitch);
+        product<PI, PI, 2, false, false, true>(kk, 0, N, sb + X::kOffK + rows, X::kTile, X::kPitch,
+                                               kn, X::kTile, X::kPitch);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int j = j0 + (n + m) * 8 + 2 * t4;
+          float from[2] = {0.f, 0.f};  // columns j and j + 1: over this thread's rows
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int i = strip * 16 + g4 + z * 8;
+            float x[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float d = i >= j + y ? decay_between(F.c[i], F.c[j + y]) : 0.f;
+              float& p = pw[n + m][2 * z + y];
+              float& q = zw[n + m][2 * z + y];
+              p = i >= j + y ? a.scale * d * p : 0.f;
+              q = i > j + y ? d * q : 0.f;
+              x[y] = i > j + y ? fmaf(p, qk[m][2 * z + y], -q * kk[m][2 * z + y]) : 0.f;
+            }
+            float upto = x[0] + x[1];
+#pragma unroll
+            for (int s = 1; s < 4; s <<= 1) {
+              const float below = __shfl_up_sync(0xffffffffu, upto, s, 4);
+              if (t4 >= s) upto += below;
+            }
+            const float here = __shfl_up_sync(0xffffffffu, upto, 1, 4);
+            const float start = before[z] + (t4 > 0 ? here : 0.f);
+            if (i >= j) from[0] += start;
+            if (i >= j + 1) from[1] += start + x[0];
+            before[z] += __shfl_sync(0xffffffffu, upto, 3, 4);
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) from[y] += __shfl_xor_sync(0xffffffffu, from[y], s);
+            if (g4 == 0) F.across[strip][j + y] = from[y];
+          }
+        }
+      }
+      if (t4 == 0) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) F.rows[slice][strip * 16 + g4 + z * 8] = before[z];
+      }
     }
     __syncthreads();  // dD's rows and de have been read: P and Z take their places
 #pragma unroll
@@ -620,17 +666,13 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
       for (int z = 0; z < 2; ++z) {
         if (n >= tiles) continue;
         const int i = strip * 16 + g4 + z * 8, j = j0 + n * 8 + 2 * t4;
-        const Decay ci = F.c[i];
-        const float d0 = i >= j ? decay_between(ci, F.c[j]) : 0.f;
-        const float d1 = i >= j + 1 ? decay_between(ci, F.c[j + 1]) : 0.f;
         uint32_t p[3];
         const int to = (i * X::kPPitch + j) * 2;
-        split2(a.scale * d0 * pw[n][2 * z], a.scale * d1 * pw[n][2 * z + 1], p[0], p[1], p[2]);
+        split2(pw[n][2 * z], pw[n][2 * z + 1], p[0], p[1], p[2]);
 #pragma unroll
         for (int x = 0; x < PP; ++x)
           *reinterpret_cast<uint32_t*>(smem + X::kOffS + x * X::kPTile + to) = p[x];
-        split2(i > j ? d0 * zw[n][2 * z] : 0.f, i > j + 1 ? d1 * zw[n][2 * z + 1] : 0.f, p[0], p[1],
-               p[2]);
+        split2(zw[n][2 * z], zw[n][2 * z + 1], p[0], p[1], p[2]);
 #pragma unroll
         for (int x = 0; x < PP; ++x)
           *reinterpret_cast<uint32_t*>(smem + X::kOffDe + x * X::kPTile + to) = p[x];
@@ -640,20 +682,14 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
     const uint32_t prow = at_rows(lane, X::kPPitch) + uint32_t(strip * 16 * X::kPPitch) * 2u;
     const uint32_t pcol = at_tokens(lane, X::kPPitch) + uint32_t(strip * 16) * 2u;
     const int below = strip * 16, upto = strip * 16 + 16;
-    product<PP, PI, NT, false, true, true>(q1, 0, upto, sb + X::kOffS + prow, X::kPTile, X::kPPitch,
-                                           sb + X::kOffK + cols, X::kTile, X::kPitch);
+    product<PP, PI, NT, false, true, kExact>(q1, 0, upto, sb + X::kOffS + prow, X::kPTile,
+                                             X::kPPitch, sb + X::kOffK + cols, X::kTile, X::kPitch);
     product<PP, PI, NT, true, true, kExact>(k2, below, L, sb + X::kOffS + pcol, X::kPTile,
                                             X::kPPitch, sb + X::kOffQ + cols, X::kTile, X::kPitch);
     product<PP, PI, NT, false, true, kExact>(k1, 0, upto, sb + X::kOffDe + prow, X::kPTile,
                                              X::kPPitch, sb + X::kOffK + cols, X::kTile, X::kPitch);
     product<PP, PI, NT, true, true, kExact>(k1, below, L, sb + X::kOffDe + pcol, X::kPTile,
                                             X::kPPitch, sb + X::kOffK + cols, X::kTile, X::kPitch);
-    float read[2];
-    dot_rows(q1, X::kOffQ, read);
-    if (t4 == 0) {
-#pragma unroll
-      for (int z = 0; z < 2; ++z) F.read[slice][strip * 16 + g4 + z * 8] = read[z];
-    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -668,25 +704,58 @@ __global__ void __launch_bounds__(Chunk<T, N>::kThreads, Chunk<T, N>::kCtas)
       put_rows(b.dq, q1);
       put_rows(b.dk, k2);
     }
-    __syncthreads();
+    // (everything that dg takes was written before the last two barriers)
     if (warp == 0) {
-      // dg: the sums over later tokens of the chunk, on top of <dD, S_L>
-      float base = 0.f, carry = 0.f;
-      for (int w = 0; w < X::kWarps; ++w) base += F.inner[w];
-#pragma unroll
-      for (int s = L - 32; s >= 0; s -= 32) {
-        const int t = s + lane;
-        float x = -F.written[t];
-#pragma unroll
-        for (int w = 0; w < X::kSlices; ++w) x += F.read[w][t];
+      constexpr int kHalves = L / 32;  // 32 tokens at a time, one a lane
+      float dg[kHalves], inner_all = 0.f;
+      for (int w = 0; w < X::kWarps; ++w) inner_all += F.inner[w];
+      const float through = F.since[L - 1] * inner_all;
+      auto from_here = [&](float x) {
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const float above = __shfl_down_sync(0xffffffffu, x, d);
           if (lane + d < 32) x += above;
         }
-        x += carry;
-        carry = __shfl_sync(0xffffffffu, x, 0);
-        if (t < len) b.dg[(t0 + t) * a.H + h] = starts || t > 0 ? base + x : 0.f;
+        return x;
+      };
+      // R over the tokens from t, X over the rows from t and the shares before t's
+      float later = 0.f, later_rows[X::kShares];
+#pragma unroll
+      for (int r = 0; r < X::kShares; ++r) later_rows[r] = 0.f;
+#pragma unroll
+      for (int s = kHalves - 1; s >= 0; --s) {
+        const int t = s * 32 + lane;
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < X::kSlices; ++w) x += F.read[w][t];
+        x = from_here(x) + later;
+        later = __shfl_sync(0xffffffffu, x, 0);
+        for (int w = t / 16; w < L / 16; ++w) x += F.across[w][t];
+#pragma unroll
+        for (int r = 0; r < X::kShares - 1; ++r) {
+          const float over = from_here(F.rows[r][t]) + later_rows[r];
+          later_rows[r] = __shfl_sync(0xffffffffu, over, 0);
+          if (t / X::kShare > r) x += over;
+        }
+        dg[s] = x + through;
+      }
+      // W over the tokens before t
+      float earlier = 0.f;
+#pragma unroll
+      for (int s = 0; s < kHalves; ++s) {
+        const int t = s * 32 + lane;
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < X::kSlices; ++w) x += F.wrote[w][t];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const float below = __shfl_up_sync(0xffffffffu, x, d);
+          if (lane >= d) x += below;
+        }
+        const float before = __shfl_up_sync(0xffffffffu, x, 1);
+        dg[s] += earlier + (lane > 0 ? before : 0.f);
+        earlier += __shfl_sync(0xffffffffu, x, 31);
+        if (t < len) b.dg[(t0 + t) * a.H + h] = dg[s];
       }
     }
   }

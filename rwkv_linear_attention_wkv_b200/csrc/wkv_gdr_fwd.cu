@@ -175,8 +175,6 @@ __global__ void __launch_bounds__(Shape<T, N, NC, NG, NP>::kThreads, CTAS)
     return;
   }
   if (!last_span) return;
-  if (checkpoints != nullptr && len > 0)
-    put_state<N>(checkpoints + int64_t((len + kChunk - 1) / kChunk) * a.H * N * N, S, lane);
   if (a.s1 != nullptr)
     put_state<N>(a.s1 + (int64_t(sp.seq) * a.H + h) * N * N + r0 * N, S, lane);
 }

@@ -177,14 +177,14 @@ int64_t gdr_plan_segments(const GdrArgs& a, GdrSegs* segs);
 int launch_gdr_combine(const GdrArgs& a, const GdrSegs& segs, bool reverse, cudaStream_t stream);
 // In groups of 16 tokens on the matrix units. e (tokens, H, N) and checkpoints (chunks, H, N, N)
 // are what the backward reads: every token's error before its write, and the state entering
-// every chunk of gdr_chunk() tokens of every sequence, and leaving the last; null = not wanted.
+// every chunk of gdr_chunk() tokens of every sequence; null = not wanted.
 int launch_gdr_chunked(const GdrArgs& a, const GdrSegs& segs, float* e, float* checkpoints,
                        cudaStream_t stream);
 // Tokens of a chunk: 32 where the chunk's operands would not fit shared memory at 64.
 __host__ __device__ constexpr int gdr_chunk(bool bf16, int N) { return !bf16 && N == 128 ? 32 : 64; }
-// Number of a sequence's first chunk. After a sequence's chunks comes one that holds the state
-// leaving the last; a packed sequence has two chunks more than whole ones, so that the numbers
-// follow from the offsets alone (which must not decrease).
+// Number of a sequence's first chunk. A packed sequence has two numbers more than whole chunks, so
+// that they follow from the offsets alone (which must not decrease); a batch row has one more than
+// chunks, which nothing is kept under.
 __host__ __device__ inline int64_t gdr_chunk_base(const GdrArgs& a, int seq, int64_t first_token) {
   const int chunk = gdr_chunk(a.bf16, a.N);
   return a.offsets == nullptr ? int64_t(seq) * ((int64_t(a.T) + chunk - 1) / chunk + 1)
