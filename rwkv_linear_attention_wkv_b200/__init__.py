@@ -104,6 +104,23 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _made(stream, make):
+    """make(), a tensor for a call on `stream` (None: the current one), from that stream's memory:
+    a block of the current stream's that is free to take may still be read there by what was
+    enqueued before. The caller works with the tensor on the current stream, so its memory stays
+    taken until that stream has passed as well, however soon the caller lets go of it."""
+    if stream is None:
+        return make()
+    cuda = _torch().cuda
+    here = cuda.current_stream(stream.device)
+    if stream == here:
+        return make()
+    with cuda.stream(stream):
+        t = make()
+    t.record_stream(here)
+    return t
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 

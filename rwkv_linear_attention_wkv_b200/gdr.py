@@ -1,7 +1,9 @@
 """Binding of the gated delta rule (include/wkv.h, wkv_gdr_*): argument marshalling only.
 
 The tensors of a call must be on one device; the call runs there, on that device's current
-stream (or the stream given), whichever device is current.
+stream (or the stream given), whichever device is current. What a call on a given stream makes
+(results without a tensor to go to, scratch) comes from that stream's memory; tensors that the
+caller made on another stream and lets go of before the call has run are the caller's to keep.
 
 An ordinary call on the current stream goes through _binding.so (csrc/binding.cpp), which returns
 NotImplemented for whatever it does not take; the functions here then check, explain and call.
@@ -12,7 +14,7 @@ import ctypes
 
 import torch
 
-from . import LIB_PATH, WkvError, lib
+from . import LIB_PATH, WkvError, _made, lib
 
 try:
     from . import _binding
@@ -64,6 +66,8 @@ def _need(t, name, dtype, shape, index):
 
 def _run(fn, index, stream, *args):
     """Calls fn(*args, stream) with CUDA device `index` current."""
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"stream must be of cuda:{index}, like the tensors, got {stream.device}")
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if index == torch._C._cuda_getDevice():
         rc = fn(*args, raw)
@@ -74,17 +78,10 @@ def _run(fn, index, stream, *args):
         raise WkvError(fn.__name__, rc)
 
 
-def _on(t, stream):
-    """t, made here for a call on `stream` (None: the current one): its memory stays taken until
-    that stream has passed the call, however soon the caller lets go of it."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def _scratch(nbytes, index, stream):
     """Uninitialised bytes for one call."""
-    return _on(torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index)), stream)
+    return _made(stream, lambda: torch.empty(nbytes, dtype=torch.uint8,
+                                             device=torch.device("cuda", index)))
 
 
 def _bytes(fn, problem, index):
@@ -138,7 +135,7 @@ def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_sta
     p, index = _problem(q, v, 2, scale, seq_offsets)
     _inputs(q, k, v, g, beta, index)
     if y is None:
-        y = _on(torch.empty_like(v), stream)
+        y = _made(stream, lambda: torch.empty_like(v))
     else:
         _need(y, "y", v.dtype, v.shape, index)
     B, T, H, N = v.shape
@@ -148,7 +145,7 @@ def _forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out, want_sta
     if not want_state:
         state_out = None
     elif state_out is None:
-        state_out = _on(v.new_empty(states, dtype=_F32), stream)
+        state_out = _made(stream, lambda: v.new_empty(states, dtype=_F32))
     else:
         _need(state_out, "state_out", _F32, states, index)
     scratch = None
@@ -234,12 +231,10 @@ def wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=None, scale=1.0
     if grad_state is not None:
         _need(grad_state, "grad_state", _F32, states, index)
     if grads is None:
-        grads = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
-                 "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
+        grads = {n: _made(stream, lambda: torch.empty_like(t)) for n, t in
+                 (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))}
         if want_dstate:
-            grads["dstate"] = v.new_empty(states, dtype=_F32)
-        for t in grads.values():
-            _on(t, stream)
+            grads["dstate"] = _made(stream, lambda: v.new_empty(states, dtype=_F32))
     else:
         for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
             _need(grads.get(n), n, t.dtype, t.shape, index)
@@ -287,7 +282,7 @@ def wkv_gdr_decode_step(q, k, v, g, beta, state, slots=None, scale=1.0, y=None, 
     elif n_slots < n:
         raise ValueError(f"state must have at least {n} slots, got {n_slots}")
     if y is None:
-        y = _on(torch.empty_like(v), stream)
+        y = _made(stream, lambda: torch.empty_like(v))
     else:
         _need(y, "y", v.dtype, v.shape, index)
     _run(lib.wkv_gdr_decode_step, index, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(),

@@ -9,8 +9,8 @@ import ctypes
 
 import torch
 
-from . import lib
-from .gdr import _binding, _DTYPES, _F32, _at, _buffer, _need, _on, _run
+from . import _made, lib
+from .gdr import _binding, _DTYPES, _F32, _at, _buffer, _need, _run
 
 _ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
 
@@ -65,14 +65,14 @@ def wkv_norm_gate_forward(h, weight=None, gate=None, x=None, scale=None, next_we
     p, index = _problem(h, weight, gate, x, scale, next_weight, group, act, eps)
     dt = h.dtype
     if out is None:
-        out = _on(torch.empty_like(h), stream)
+        out = _made(stream, lambda: torch.empty_like(h))
     else:
         _need(out, "out", dt, h.shape, index)
     if next_weight is None:
         if y is not None:
             raise ValueError("y needs next_weight")
     elif y is None:
-        y = _on(torch.empty_like(h), stream)
+        y = _made(stream, lambda: torch.empty_like(h))
     else:
         _need(y, "y", dt, h.shape, index)
     _run(lib.wkv_norm_gate_forward, index, stream, ctypes.byref(p), h.data_ptr(), _at(weight), _at(gate),
@@ -103,7 +103,7 @@ def wkv_norm_gate_backward(h, weight, dout, gate=None, x=None, scale=None, next_
     for n, t in (("dout", dout), ("dy", dy)):
         if t is not None:
             _need(t, n, dt, h.shape, index)
-    like = lambda t: None if t is None else _on(torch.empty_like(t), stream)  # noqa: E731
+    like = lambda t: None if t is None else _made(stream, lambda: torch.empty_like(t))  # noqa: E731
     g = {"dh": like(h), "dweight": like(weight), "dgate": like(gate), "dx": like(x),
          "dscale": like(scale), "dnext_weight": None if dy is None else like(next_weight)}
     workspace = _buffer(workspace, "workspace", wkv_norm_gate_workspace_bytes(p.R, p.C), index,

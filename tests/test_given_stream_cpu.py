@@ -1,0 +1,50 @@
+"""Memory that the bindings make for a call on a given stream, without a GPU: it is that stream's."""
+import contextlib
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class Stream:
+    device, device_index, cuda_stream = torch.device("cuda", 0), 0, 7
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """(the stream given, what was made under which stream, the streams recorded)."""
+    given, here, inside, made, recorded = Stream(), Stream(), [], [], []
+
+    @contextlib.contextmanager
+    def on(s):
+        inside.append(s)
+        yield
+        inside.pop()
+
+    empty = torch.empty
+
+    def make(*args, device=None, **kw):
+        made.append(inside[-1] if inside else here)
+        return empty(*args, **kw)
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: here)
+    monkeypatch.setattr(torch, "empty", make)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append(s))
+    return given, here, made, recorded
+
+
+def test_scratch_is_the_streams(streams):
+    from rwkv_linear_attention_wkv_b200 import gdr
+    given, here, made, recorded = streams
+    gdr._scratch(64, 0, given)
+    assert made == [given] and recorded == [here]
+    gdr._scratch(64, 0, None)
+    gdr._scratch(64, 0, here)
+    assert made == [given, here, here] and recorded == [here]
+
+
+def test_a_stream_of_another_device_is_refused():
+    from rwkv_linear_attention_wkv_b200 import gdr
+    with pytest.raises(ValueError, match="stream must be of cuda:1"):
+        gdr._run(None, 1, Stream())
