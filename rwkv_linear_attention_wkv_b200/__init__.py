@@ -121,6 +121,10 @@ def _made(stream, make):
     return t
 
 
+def _empty(stream, shape, dtype, device):
+    return _made(stream, lambda: _torch().empty(shape, dtype=dtype, device=device))
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -153,7 +157,7 @@ def _call(fn, *args):
         raise WkvError(fn, rc)
 
 
-def _fwd_common(w, u, k, v, r, y, dtype):
+def _fwd_common(w, u, k, v, r, y, dtype, stream):
     torch = _torch()
     if not _dims(k, "k", 3):
         raise ValueError("k must be (B, T, C)")
@@ -165,7 +169,7 @@ def _fwd_common(w, u, k, v, r, y, dtype):
     _need(w, "w", torch.float32, (C,))
     _need(u, "u", torch.float32, (C,))
     if y is None:
-        y = torch.empty((B, T, C), dtype=dtype, device=k.device)
+        y = _empty(stream, (B, T, C), dtype=dtype, device=k.device)
     _need(y, "y", dtype, (B, T, C))
     return B, T, C, y
 
@@ -173,7 +177,7 @@ def _fwd_common(w, u, k, v, r, y, dtype):
 def wkv_forward(w, u, k, v, r=None, y=None, stream=None):
     """fp32 forward: y = sigmoid(r) * wkv (no gate when r is None). Returns y."""
     torch = _torch()
-    B, T, C, y = _fwd_common(w, u, k, v, r, y, torch.float32)
+    B, T, C, y = _fwd_common(w, u, k, v, r, y, torch.float32, stream)
     _call("wkv_forward", B, T, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r), _ptr(y),
           _stream(stream))
     return y
@@ -182,7 +186,7 @@ def wkv_forward(w, u, k, v, r=None, y=None, stream=None):
 def wkv_forward_bf16(w, u, k, v, r=None, y=None, stream=None):
     """bf16 in/out forward (fp32 arithmetic). Returns y (bf16)."""
     torch = _torch()
-    B, T, C, y = _fwd_common(w, u, k, v, r, y, torch.bfloat16)
+    B, T, C, y = _fwd_common(w, u, k, v, r, y, torch.bfloat16, stream)
     _call("wkv_forward_bf16", B, T, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r), _ptr(y),
           _stream(stream))
     return y
@@ -196,7 +200,7 @@ def wkv_forward_state(w, u, k, v, r=None, state=None, y=None, state_out=None,
     (and may be the same tensors as state) to write the final state in place.
     """
     torch = _torch()
-    B, T, C, y = _fwd_common(w, u, k, v, r, y, torch.float32)
+    B, T, C, y = _fwd_common(w, u, k, v, r, y, torch.float32, stream)
     a0 = b0 = p0 = None
     if state is not None:
         a0, b0, p0 = state
@@ -205,7 +209,7 @@ def wkv_forward_state(w, u, k, v, r=None, state=None, y=None, state_out=None,
     a1 = b1 = p1 = None
     if want_state:
         if state_out is None:
-            state_out = tuple(torch.empty((B, C), dtype=torch.float32, device=k.device)
+            state_out = tuple(_empty(stream, (B, C), dtype=torch.float32, device=k.device)
                               for _ in range(3))
         a1, b1, p1 = state_out
         for n, t in (("a1", a1), ("b1", b1), ("p1", p1)):
@@ -230,7 +234,7 @@ def wkv_decode_step(w, u, k, v, r, a, b, p, y=None, stream=None):
     _need(w, "w", f32, (L, C))
     _need(u, "u", f32, (L, C))
     if y is None:
-        y = torch.empty((N, L, C), dtype=f32, device=k.device)
+        y = _empty(stream, (N, L, C), dtype=f32, device=k.device)
     _need(y, "y", f32, (N, L, C))
     _call("wkv_decode_step", N, L, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r), _ptr(y),
           _ptr(a), _ptr(b), _ptr(p), _stream(stream))
@@ -254,7 +258,7 @@ def wkv_decode_steps(w, u, k, v, r, a, b, p, y=None, stream=None):
     _need(w, "w", f32, (L, C))
     _need(u, "u", f32, (L, C))
     if y is None:
-        y = torch.empty((S, N, L, C), dtype=f32, device=k.device)
+        y = _empty(stream, (S, N, L, C), dtype=f32, device=k.device)
     _need(y, "y", f32, (S, N, L, C))
     _call("wkv_decode_steps", N, L, C, S, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r),
           _ptr(y), _ptr(a), _ptr(b), _ptr(p), _stream(stream))
@@ -290,17 +294,17 @@ def wkv_backward(w, u, k, v, r, dy, want_dr=True, workspace=None, out=None, stre
     dev = k.device
     for n, shape in (("dk", (B, T, C)), ("dv", (B, T, C)), ("dw", (C,)), ("du", (C,))):
         if out.get(n) is None:
-            out[n] = torch.empty(shape, dtype=f32, device=dev)
+            out[n] = _empty(stream, shape, dtype=f32, device=dev)
         _need(out[n], n, f32, shape)
     if r is not None and want_dr:
         if out.get("dr") is None:
-            out["dr"] = torch.empty((B, T, C), dtype=f32, device=dev)
+            out["dr"] = _empty(stream, (B, T, C), dtype=f32, device=dev)
         _need(out["dr"], "dr", f32, (B, T, C))
     else:
         out["dr"] = None
     nbytes = wkv_backward_workspace_bytes(B, T, C)
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, nbytes, dtype=torch.uint8, device=dev)
     if not workspace.is_cuda or workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace must be a CUDA tensor of at least {nbytes} bytes")
     _call(_entry, B, T, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r), _ptr(dy),
@@ -340,17 +344,17 @@ def wkv_backward_state(w, u, k, v, r, dy, state=None, grad_state=None, want_dr=T
     for n, shape in (("dk", (B, T, C)), ("dv", (B, T, C)), ("dw", (C,)), ("du", (C,)),
                      ("da0", (B, C)), ("db0", (B, C)), ("dp0", (B, C))):
         if out.get(n) is None:
-            out[n] = torch.empty(shape, dtype=f32, device=dev)
+            out[n] = _empty(stream, shape, dtype=f32, device=dev)
         _need(out[n], n, f32, shape)
     if r is not None and want_dr:
         if out.get("dr") is None:
-            out["dr"] = torch.empty((B, T, C), dtype=f32, device=dev)
+            out["dr"] = _empty(stream, (B, T, C), dtype=f32, device=dev)
         _need(out["dr"], "dr", f32, (B, T, C))
     else:
         out["dr"] = None
     nbytes = wkv_backward_workspace_bytes(B, T, C)
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, nbytes, dtype=torch.uint8, device=dev)
     if not workspace.is_cuda or workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace must be a CUDA tensor of at least {nbytes} bytes")
     _call(_entry, B, T, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r), _ptr(dy),
@@ -386,11 +390,11 @@ def wkv_forward_checkpointed(w, u, k, v, r=None, state=None, y=None, workspace=N
         if t is not None:
             _need(t, n, f32, (B, C))
     if y is None:
-        y = torch.empty((B, T, C), dtype=f32, device=k.device)
+        y = _empty(stream, (B, T, C), dtype=f32, device=k.device)
     _need(y, "y", f32, (B, T, C))
     nbytes = wkv_backward_workspace_bytes(B, T, C)
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=k.device)
+        workspace = _empty(stream, nbytes, dtype=torch.uint8, device=k.device)
     if not workspace.is_cuda or workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace must be a CUDA tensor of at least {nbytes} bytes")
     _call("wkv_forward_checkpointed", B, T, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r),
@@ -423,14 +427,14 @@ def wkv7_forward(r, w, k, v, a, b, state=None, y=None, state_out=None, want_stat
     for n, t in (("r", r), ("w", w), ("k", k), ("v", v), ("a", a), ("b", b)):
         _need(t, n, f32, (B, T, H, N))
     if y is None:
-        y = torch.empty((B, T, H, N), dtype=f32, device=k.device)
+        y = _empty(stream, (B, T, H, N), dtype=f32, device=k.device)
     _need(y, "y", f32, (B, T, H, N))
     if state is not None:
         _need(state, "state", f32, (B, H, N, N))
     s1 = None
     if want_state:
-        s1 = state_out if state_out is not None else torch.empty((B, H, N, N), dtype=f32,
-                                                                 device=k.device)
+        s1 = state_out if state_out is not None else _empty(
+            stream, (B, H, N, N), dtype=f32, device=k.device)
         _need(s1, "state_out", f32, (B, H, N, N))
     _call("wkv7_forward", B, T, H, N, _ptr(r), _ptr(w), _ptr(k), _ptr(v), _ptr(a), _ptr(b),
           _ptr(y), _ptr(state), _ptr(s1), _stream(stream))
@@ -450,14 +454,14 @@ def wkv_mstate_forward(r, w, k, v, state=None, y=None, state_out=None, want_stat
     for n, t in (("r", r), ("w", w), ("k", k), ("v", v)):
         _need(t, n, f32, (B, T, H, N))
     if y is None:
-        y = torch.empty((B, T, H, N), dtype=f32, device=k.device)
+        y = _empty(stream, (B, T, H, N), dtype=f32, device=k.device)
     _need(y, "y", f32, (B, T, H, N))
     if state is not None:
         _need(state, "state", f32, (B, H, N, N))
     s1 = None
     if want_state:
-        s1 = state_out if state_out is not None else torch.empty((B, H, N, N), dtype=f32,
-                                                                 device=k.device)
+        s1 = state_out if state_out is not None else _empty(
+            stream, (B, H, N, N), dtype=f32, device=k.device)
         _need(s1, "state_out", f32, (B, H, N, N))
     _call("wkv_mstate_forward", B, T, H, N, _ptr(r), _ptr(w), _ptr(k), _ptr(v), _ptr(y),
           _ptr(state), _ptr(s1), _stream(stream))

@@ -65,3 +65,27 @@ def test_the_norms(W):
     check(lambda s: W.wkv_norm_gate_forward(h, w, gate=z, x=x, next_weight=w, stream=s))
     check(lambda s: W.wkv_norm_gate_backward(h, w, x, gate=z, x=x, next_weight=w, dy=z, stream=s),
           [W.wkv_norm_gate_workspace_bytes(500, 256)])
+
+
+def test_the_channel_operators(W):
+    B, T, C = 2, 64, 64
+    r = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+    w, u = 0.1 + torch.rand(C, device="cuda"), r(C)
+    k, v, g, dy = (r(B, T, C) for _ in range(4))
+    ws = W.wkv_backward_workspace_bytes(B, T, C)
+    check(lambda s: W.wkv_forward(w, u, k, v, g, stream=s))
+    half = [t.to(BF16) for t in (k, v, g)]
+    check(lambda s: W.wkv_forward_bf16(w, u, *half, stream=s))
+    check(lambda s: W.wkv_forward_state(w, u, k, v, g, stream=s))
+    check(lambda s: W.wkv_backward(w, u, k, v, g, dy, stream=s), [ws])
+    _, kept = W.wkv_forward_checkpointed(w, u, k, v, g)
+    check(lambda s: W.wkv_forward_checkpointed(w, u, k, v, g, stream=s)[0], [ws])
+    check(lambda s: W.wkv_backward_checkpointed(w, u, k, v, g, dy, kept, stream=s))
+
+
+def test_the_matrix_states(W):
+    r, k, v = (0.3 * torch.randn(1, 70, 2, 64, device="cuda") for _ in range(3))
+    w = 0.5 + 0.5 * torch.rand(1, 70, 2, 64, device="cuda")
+    check(lambda s: W.wkv_mstate_forward(r, w, k, v, stream=s))
+    a, b = -0.1 * k, 0.1 * k
+    check(lambda s: W.wkv7_forward(r, w, k, v, a, b, stream=s))
