@@ -75,6 +75,18 @@ WKV_API int wkv_testing_backward_state_plain(
     float* dw, float* du, float* dr, float* da0, float* db0, float* dp0, void* workspace,
     size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * The next n kernel launches of this thread by this library are made and then reported as failed
+ * (the calls return WKV_ERR_CUDA). Lets tests see that a caller does not make such a call again.
+ */
+WKV_API int wkv_testing_fail_launches(int n);
+
+/*
+ * Leaves a CUDA error of this thread unasked for, as a refused allocation does (the attribute of a
+ * device that there is not). No later call may report it as its own.
+ */
+WKV_API int wkv_testing_leave_error(void);
+
 /* Pipes wkv_testing_pipe_rate can measure. */
 #define WKV_PIPE_EX2 0   /* ex2.approx.ftz.f32 instructions per second (MUFU) */
 #define WKV_PIPE_FFMA2 1 /* fp32 flops per second through packed fp32x2 FMA (4 per instruction) */

@@ -69,6 +69,8 @@ _SIGS = {
     "wkv_norm_gate_workspace_bytes": ([_I, _I], ctypes.c_size_t),
     "wkv_norm_gate_backward": ([_P] * 16 + [ctypes.c_size_t, _P], ctypes.c_int),
     "wkv_testing_set_backward_path": ([ctypes.c_int], ctypes.c_int),
+    "wkv_testing_fail_launches": ([ctypes.c_int], ctypes.c_int),
+    "wkv_testing_leave_error": ([], ctypes.c_int),
     "wkv_testing_pipe_rate": ([ctypes.c_int, _I, ctypes.POINTER(ctypes.c_double), _P],
                               ctypes.c_int),
 }

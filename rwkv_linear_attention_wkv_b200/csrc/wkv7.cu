@@ -242,9 +242,8 @@ int launch_wkv7(int64_t B, int64_t T, int64_t H, const float* r, const float* w,
   if (cudaFuncSetAttribute(wkv7_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            int(smem)) != cudaSuccess)
     return WKV_ERR_CUDA;
-  wkv7_fwd_kernel<<<unsigned(B * H), kThr7, smem, stream>>>(m, int(B), int(T), int(H), s0, s1,
-                                                            err);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(wkv7_fwd_kernel, unsigned(B * H), kThr7, smem, stream, m, int(B), int(T),
+                       int(H), s0, s1, err);
 }
 
 }  // namespace wkv

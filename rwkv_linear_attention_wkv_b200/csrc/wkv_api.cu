@@ -408,6 +408,18 @@ WKV_API int wkv_stream_status(cudaStream_t stream) {
   return WKV_OK;
 }
 
+WKV_API int wkv_testing_fail_launches(int n) {
+  if (n < 0) return WKV_ERR_INVALID_ARG;
+  failing_launches = n;
+  return WKV_OK;
+}
+
+WKV_API int wkv_testing_leave_error(void) {
+  int value = 0;
+  return cudaDeviceGetAttribute(&value, cudaDevAttrWarpSize, -1) == cudaSuccess ? WKV_ERR_INVALID_ARG
+                                                                                : WKV_OK;
+}
+
 WKV_API int wkv_testing_lookback_timeout(uint64_t wait_ns, cudaStream_t stream) {
   const int64_t B = 1, T = 768, C = 32;
   int64_t flag_bytes = 0;

@@ -1650,10 +1650,9 @@ int launch_main(const BwdArgs& a, const TensorMaps4& in, const TensorMaps4& out,
       cudaSuccess)
     return WKV_ERR_CUDA;
   const int64_t grid = a.B * ((a.C + 31) / 32);
-  kern<<<unsigned(grid), 32, smem, stream>>>(in, out, a.k, a.v, a.r, a.dy, a.dk, a.dv, a.dr,
-                                             int(a.B), int(a.T), int(a.C), a.w, a.u,
-                                             state_io(a), a.ws, a.err);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(kern, unsigned(grid), 32, smem, stream, in, out, a.k, a.v, a.r, a.dy, a.dk,
+                       a.dv, a.dr, int(a.B), int(a.T), int(a.C), a.w, a.u, state_io(a), a.ws,
+                       a.err);
 }
 
 template <bool GATE, bool DR>
@@ -1665,10 +1664,9 @@ int launch_seg(const BwdArgs& a, const TensorMaps4& in, const TensorMaps4& out, 
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
       cudaSuccess)
     return WKV_ERR_CUDA;
-  kern<<<unsigned(nitems), kSW * 32, smem, stream>>>(in, out, int(a.B), int(a.T), int(a.C), a.w,
-                                                      a.u, state_io(a), a.ws, a.err, a.wait_ns,
-                                                      a.withhold_last_map);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(kern, unsigned(nitems), kSW * 32, smem, stream, in, out, int(a.B), int(a.T),
+                       int(a.C), a.w, a.u, state_io(a), a.ws, a.err, a.wait_ns,
+                       a.withhold_last_map);
 }
 
 // Reverse pass with one CTA per channel group: taken when there are enough groups to fill
@@ -1700,10 +1698,9 @@ int launch_group_nw(const BwdArgs& a, const TensorMaps4& in, const TensorMaps4& 
       cudaSuccess)
     return WKV_ERR_CUDA;
   const Ptr4 pre{a.k, a.v, a.r ? a.r : a.dy, a.dy};
-  kern<<<unsigned(a.B * ((a.C + 31) / 32)), NW * 32, smem, stream>>>(
-      in, out, int(a.B), int(a.T), int(a.C), a.w, a.u, state_io(a), a.ws, a.err, pre, a.dw,
-      a.du);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(kern, unsigned(a.B * ((a.C + 31) / 32)), NW * 32, smem, stream, in, out,
+                       int(a.B), int(a.T), int(a.C), a.w, a.u, state_io(a), a.ws, a.err, pre, a.dw,
+                       a.du);
 }
 
 // Five warps (five chunks an iteration, 3 CTAs per SM at 128 registers) while every group's
@@ -1755,13 +1752,13 @@ int launch_all(const BwdArgs& a, cudaStream_t stream) {
       const int64_t citems = grid * ((nch + kSW * kCK - 1) / (kSW * kCK));
       if (group) {
         const Ptr4 pre{a.k, a.v, a.k, a.v};
-        wkv_bwd_ckpt_group_kernel<<<unsigned(grid), kSW * 32, 0, stream>>>(
-            ck, int(a.B), int(a.T), int(a.C), a.w, state_io(a), a.ws, a.err, pre);
+        rc = launch_kernel(wkv_bwd_ckpt_group_kernel, unsigned(grid), kSW * 32, 0, stream, ck,
+                           int(a.B), int(a.T), int(a.C), a.w, state_io(a), a.ws, a.err, pre);
       } else {
-        wkv_bwd_ckpt_seg_kernel<<<unsigned(citems), kSW * 32, 0, stream>>>(
-            ck, int(a.B), int(a.T), int(a.C), a.w, state_io(a), a.ws, a.err, a.wait_ns);
+        rc = launch_kernel(wkv_bwd_ckpt_seg_kernel, unsigned(citems), kSW * 32, 0, stream, ck,
+                           int(a.B), int(a.T), int(a.C), a.w, state_io(a), a.ws, a.err, a.wait_ns);
       }
-      if (cudaPeekAtLastError() != cudaSuccess) return WKV_ERR_CUDA;
+      if (rc != WKV_OK) return rc;
     }
     if (group) {
       if (a.r)
@@ -1776,10 +1773,9 @@ int launch_all(const BwdArgs& a, cudaStream_t stream) {
       rc = launch_seg<false, false>(a, in, out, nitems, stream);
     }
   } else {
-    wkv_bwd_ckpt_kernel<TMA><<<unsigned(grid), 32, 0, stream>>>(ck, a.k, a.v, int(a.B), int(a.T),
-                                                                int(a.C), a.w, state_io(a), a.ws,
-                                                                a.err);
-    if (cudaPeekAtLastError() != cudaSuccess) return WKV_ERR_CUDA;
+    rc = launch_kernel(wkv_bwd_ckpt_kernel<TMA>, unsigned(grid), 32, 0, stream, ck, a.k, a.v,
+                       int(a.B), int(a.T), int(a.C), a.w, state_io(a), a.ws, a.err);
+    if (rc != WKV_OK) return rc;
     if (a.r)
       rc = a.dr ? launch_main<TMA, true, true>(a, in, out, stream)
                 : launch_main<TMA, true, false>(a, in, out, stream);
@@ -1787,9 +1783,8 @@ int launch_all(const BwdArgs& a, cudaStream_t stream) {
       rc = launch_main<TMA, false, false>(a, in, out, stream);
   }
   if (rc || group) return rc;  // (the per-group reverse pass writes dw, du itself)
-  wkv_bwd_reduce_kernel<<<unsigned((a.C + 31) / 32), dim3(32, kRS), 0, stream>>>(
-      int(a.B), int(a.C), a.ws, int(a.T), a.dw, a.du);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(wkv_bwd_reduce_kernel, unsigned((a.C + 31) / 32), dim3(32, kRS), 0, stream,
+                       int(a.B), int(a.C), a.ws, int(a.T), a.dw, a.du);
 }
 
 }  // namespace
@@ -1824,8 +1819,8 @@ __global__ void wkv_bwd_no_tokens_kernel(int64_t n, const StateIO io) {
 
 int launch_backward_no_tokens(const BwdArgs& a, cudaStream_t stream) {
   const int64_t n = a.B * a.C;
-  wkv_bwd_no_tokens_kernel<<<unsigned((n + 255) / 256), 256, 0, stream>>>(n, state_io(a));
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(wkv_bwd_no_tokens_kernel, unsigned((n + 255) / 256), 256, 0, stream, n,
+                       state_io(a));
 }
 
 bool backward_time_parallel_ok(const BwdArgs& a) {

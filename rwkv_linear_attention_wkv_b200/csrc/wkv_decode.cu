@@ -179,23 +179,22 @@ int launch_decode_steps(const DecodeArgs& d, int64_t S, cudaStream_t stream) {
     auto m4 = [](float* q) { return reinterpret_cast<float4*>(q); };
     const int64_t LC4 = d.L * d.C / 4;
     if (gate)
-      wkv_decode_steps_vec4_kernel<true><<<unsigned(grid), block, 0, stream>>>(
-          items, LC4, s32, f4(d.w), f4(d.u), f4(d.k), f4(d.v), f4(d.r), m4(d.y), m4(d.a),
-          m4(d.b), m4(d.p));
+      return launch_kernel(wkv_decode_steps_vec4_kernel<true>, unsigned(grid), block, 0, stream,
+                           items, LC4, s32, f4(d.w), f4(d.u), f4(d.k), f4(d.v), f4(d.r), m4(d.y),
+                           m4(d.a), m4(d.b), m4(d.p));
     else
-      wkv_decode_steps_vec4_kernel<false><<<unsigned(grid), block, 0, stream>>>(
-          items, LC4, s32, f4(d.w), f4(d.u), f4(d.k), f4(d.v), nullptr, m4(d.y), m4(d.a),
-          m4(d.b), m4(d.p));
+      return launch_kernel(wkv_decode_steps_vec4_kernel<false>, unsigned(grid), block, 0, stream,
+                           items, LC4, s32, f4(d.w), f4(d.u), f4(d.k), f4(d.v), nullptr, m4(d.y),
+                           m4(d.a), m4(d.b), m4(d.p));
   } else {
     const int64_t LC = d.L * d.C;
     if (gate)
-      wkv_decode_steps_scalar_kernel<true><<<unsigned(grid), block, 0, stream>>>(
-          items, LC, s32, d.w, d.u, d.k, d.v, d.r, d.y, d.a, d.b, d.p);
+      return launch_kernel(wkv_decode_steps_scalar_kernel<true>, unsigned(grid), block, 0, stream,
+                           items, LC, s32, d.w, d.u, d.k, d.v, d.r, d.y, d.a, d.b, d.p);
     else
-      wkv_decode_steps_scalar_kernel<false><<<unsigned(grid), block, 0, stream>>>(
-          items, LC, s32, d.w, d.u, d.k, d.v, nullptr, d.y, d.a, d.b, d.p);
+      return launch_kernel(wkv_decode_steps_scalar_kernel<false>, unsigned(grid), block, 0, stream,
+                           items, LC, s32, d.w, d.u, d.k, d.v, nullptr, d.y, d.a, d.b, d.p);
   }
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
 }
 
 int launch_decode(const DecodeArgs& d, cudaStream_t stream) {
@@ -219,23 +218,22 @@ int launch_decode(const DecodeArgs& d, cudaStream_t stream) {
     auto m4 = [](float* q) { return reinterpret_cast<float4*>(q); };
     const int64_t LC4 = d.L * d.C / 4;
     if (gate)
-      wkv_decode_vec4_kernel<true><<<unsigned(grid), block, 0, stream>>>(
-          items, LC4, d.C / 4, f4(d.w), f4(d.u), f4(d.k), f4(d.v), f4(d.r), m4(d.y), m4(d.a),
-          m4(d.b), m4(d.p));
+      return launch_kernel(wkv_decode_vec4_kernel<true>, unsigned(grid), block, 0, stream, items,
+                           LC4, d.C / 4, f4(d.w), f4(d.u), f4(d.k), f4(d.v), f4(d.r), m4(d.y),
+                           m4(d.a), m4(d.b), m4(d.p));
     else
-      wkv_decode_vec4_kernel<false><<<unsigned(grid), block, 0, stream>>>(
-          items, LC4, d.C / 4, f4(d.w), f4(d.u), f4(d.k), f4(d.v), nullptr, m4(d.y), m4(d.a),
-          m4(d.b), m4(d.p));
+      return launch_kernel(wkv_decode_vec4_kernel<false>, unsigned(grid), block, 0, stream, items,
+                           LC4, d.C / 4, f4(d.w), f4(d.u), f4(d.k), f4(d.v), nullptr, m4(d.y),
+                           m4(d.a), m4(d.b), m4(d.p));
   } else {
     const int64_t LC = d.L * d.C;
     if (gate)
-      wkv_decode_scalar_kernel<true><<<unsigned(grid), block, 0, stream>>>(
-          items, LC, d.w, d.u, d.k, d.v, d.r, d.y, d.a, d.b, d.p);
+      return launch_kernel(wkv_decode_scalar_kernel<true>, unsigned(grid), block, 0, stream, items,
+                           LC, d.w, d.u, d.k, d.v, d.r, d.y, d.a, d.b, d.p);
     else
-      wkv_decode_scalar_kernel<false><<<unsigned(grid), block, 0, stream>>>(
-          items, LC, d.w, d.u, d.k, d.v, nullptr, d.y, d.a, d.b, d.p);
+      return launch_kernel(wkv_decode_scalar_kernel<false>, unsigned(grid), block, 0, stream, items,
+                           LC, d.w, d.u, d.k, d.v, nullptr, d.y, d.a, d.b, d.p);
   }
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
 }
 
 }  // namespace wkv

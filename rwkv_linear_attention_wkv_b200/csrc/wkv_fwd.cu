@@ -296,9 +296,8 @@ int launch_tma(const FwdArgs& a, cudaStream_t stream, float4* ckpt = nullptr,
     return WKV_ERR_CUDA;
   const int64_t G = (a.C + CW - 1) / CW;
   const int64_t grid = a.B * G;
-  kern<<<unsigned(grid), CW, smem, stream>>>(tk, tv, tr, ty, int(a.T), int(a.C), a.w, a.u, a.a0,
-                                             a.b0, a.p0, a.a1, a.b1, a.p1, a.err, ckpt, ckend);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(kern, unsigned(grid), CW, smem, stream, tk, tv, tr, ty, int(a.T), int(a.C),
+                       a.w, a.u, a.a0, a.b0, a.p0, a.a1, a.b1, a.p1, a.err, ckpt, ckend);
 }
 
 template <typename Tin, bool GATE>
@@ -306,10 +305,10 @@ int launch_plain(const FwdArgs& a, cudaStream_t stream) {
   const int64_t n = a.B * a.C;
   const int block = 128;
   const int64_t grid = (n + block - 1) / block;
-  wkv_fwd_plain_kernel<Tin, GATE><<<unsigned(grid), block, 0, stream>>>(
-      a.B, a.T, a.C, a.w, a.u, static_cast<const Tin*>(a.k), static_cast<const Tin*>(a.v),
-      static_cast<const Tin*>(a.r), static_cast<Tin*>(a.y), a.a0, a.b0, a.p0, a.a1, a.b1, a.p1);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(wkv_fwd_plain_kernel<Tin, GATE>, unsigned(grid), block, 0, stream, a.B, a.T,
+                       a.C, a.w, a.u, static_cast<const Tin*>(a.k), static_cast<const Tin*>(a.v),
+                       static_cast<const Tin*>(a.r), static_cast<Tin*>(a.y), a.a0, a.b0, a.p0, a.a1,
+                       a.b1, a.p1);
 }
 
 template <typename Tin>

@@ -783,9 +783,8 @@ int chain(const GdrBwdArgs& b, const GdrSegs& segs, cudaStream_t stream) {
   auto* kernel = gdr_chain_kernel<T, N, 4, 2, NP, CTAS, SUMMARY>;
   if (!allow_smem(kernel, X::kSmem)) return WKV_ERR_CUDA;
   const int64_t spans = segs.tokens == 0 ? b.p.n_seqs : segs.slots;
-  kernel<<<unsigned(spans * b.p.H * (N / X::kVRows) * (SUMMARY ? 2 : 1)), X::kThreads, X::kSmem,
-           stream>>>(b, segs);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(kernel, unsigned(spans * b.p.H * (N / X::kVRows) * (SUMMARY ? 2 : 1)),
+                       X::kThreads, X::kSmem, stream, b, segs);
 }
 
 template <typename T, int N>
@@ -794,8 +793,8 @@ int rest(const GdrBwdArgs& b, cudaStream_t stream) {
   auto* kernel =
       b.p.H == b.p.Hk ? gdr_chunk_kernel<T, N, false> : gdr_chunk_kernel<T, N, true>;
   if (!allow_smem(kernel, X::kSmem)) return WKV_ERR_CUDA;
-  kernel<<<unsigned(gdr_chunks(b.p) * b.p.Hk), X::kThreads, X::kSmem, stream>>>(b);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(kernel, unsigned(gdr_chunks(b.p) * b.p.Hk), X::kThreads, X::kSmem, stream,
+                       b);
 }
 
 template <typename T, int N>

@@ -188,9 +188,8 @@ int launch(const GdrArgs& a, const GdrSegs& segs, float* e, float* checkpoints,
       cudaSuccess)
     return WKV_ERR_CUDA;
   const int64_t spans = segs.tokens == 0 ? a.n_seqs : segs.slots;
-  kernel<<<unsigned(spans * a.H * (N / X::kVRows) * (SUMMARY ? 2 : 1)), X::kThreads, X::kSmem,
-           stream>>>(a, segs, e, checkpoints);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(kernel, unsigned(spans * a.H * (N / X::kVRows) * (SUMMARY ? 2 : 1)),
+                       X::kThreads, X::kSmem, stream, a, segs, e, checkpoints);
 }
 
 template <typename T, int N, int NP, int CTAS>

@@ -114,8 +114,8 @@ int combine(const GdrArgs& a, const GdrSegs& segs, bool reverse, cudaStream_t st
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
       cudaSuccess)
     return WKV_ERR_CUDA;
-  kernel<<<unsigned(a.n_seqs * a.H * (N / 64)), 128, kSmem, stream>>>(a, segs, reverse);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(kernel, unsigned(a.n_seqs * a.H * (N / 64)), 128, kSmem, stream, a, segs,
+                       reverse);
 }
 
 }  // namespace

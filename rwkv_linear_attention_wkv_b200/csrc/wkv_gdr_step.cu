@@ -120,10 +120,8 @@ int launch(const GdrArgs& a, cudaStream_t stream) {
   const int split = a.N / (kRows * kWarps);
   const unsigned grid = unsigned(int64_t(a.n_seqs) * a.H * split);
   if (a.N == 64)
-    gdr_decode_kernel<T, 64><<<grid, kWarps * 32, 0, stream>>>(a);
-  else
-    gdr_decode_kernel<T, 128><<<grid, kWarps * 32, 0, stream>>>(a);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+    return launch_kernel(gdr_decode_kernel<T, 64>, grid, kWarps * 32, 0, stream, a);
+  return launch_kernel(gdr_decode_kernel<T, 128>, grid, kWarps * 32, 0, stream, a);
 }
 
 }  // namespace

@@ -6,9 +6,33 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <utility>
+
 #include "wkv.h"
 
 namespace wkv {
+
+// For tests: launches of this thread that are still to report a failure (after they were made).
+inline thread_local int failing_launches = 0;
+
+// A launch and how that launch went. (After <<<>>> one can only ask for the thread's last error,
+// which may be an earlier call's: CUDA keeps it until somebody takes it.)
+template <typename... Params, typename... Args>
+int launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                  cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = block;
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  if (cudaLaunchKernelEx(&config, kernel, std::forward<Args>(args)...) != cudaSuccess)
+    return WKV_ERR_CUDA;
+  if (failing_launches > 0) {
+    --failing_launches;
+    return WKV_ERR_CUDA;
+  }
+  return WKV_OK;
+}
 
 // Arguments of one forward pass over (B, T, C). k, v, r, y are fp32 or bf16 according to
 // the entry point; r may be null (no gate); a0/b0/p0 null = empty initial state; a1/b1/p1

@@ -458,10 +458,9 @@ int launch_mstate(int64_t B, int64_t T, int64_t H, const float* r, const float* 
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t grid = std::min<int64_t>(BH * nch, int64_t(2) * sms);  // persistent, 2 per SM
-  wkv_mstate_kernel<<<unsigned(grid), kThreads, kSmemBytes, stream>>>(
-      r, w, k, v, y, s0, s1, int(B), int(T), int(H), int(nch), ring, flags, ticket, err,
-      kWaitLimitNs);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(wkv_mstate_kernel, unsigned(grid), kThreads, kSmemBytes, stream, r, w, k, v,
+                       y, s0, s1, int(B), int(T), int(H), int(nch), ring, flags, ticket, err,
+                       kWaitLimitNs);
 }
 
 }  // namespace wkv

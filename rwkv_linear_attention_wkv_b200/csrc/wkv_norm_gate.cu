@@ -522,8 +522,8 @@ int run(const NormGateArgs& a, const Plan& p, bool backward, cudaStream_t stream
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem)) !=
           cudaSuccess)
     return WKV_ERR_CUDA;
-  kernel<<<p.grid, p.team_warps * p.teams * 32, p.smem, stream>>>(a, p.team_warps);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(kernel, p.grid, p.team_warps * p.teams * 32, p.smem, stream, a,
+                       p.team_warps);
 }
 
 template <typename T>
@@ -575,9 +575,8 @@ int launch_norm_gate_backward(const NormGateArgs& a, cudaStream_t stream) {
                         : pick<float>(a, p, vec, true, stream);
   if (rc != WKV_OK) return rc;
   if (!a.dweight && !a.dscale && !a.dnext_weight) return WKV_OK;
-  norm_gate_sum_kernel<<<dim3((a.C + 31) / 32, 3), 32 * kSlices, 0, stream>>>(
-      a.partial, p.grid, a.C, a.dweight, a.dscale, a.dnext_weight);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(norm_gate_sum_kernel, dim3((a.C + 31) / 32, 3), 32 * kSlices, 0, stream,
+                       a.partial, p.grid, a.C, a.dweight, a.dscale, a.dnext_weight);
 }
 
 }  // namespace wkv

@@ -81,10 +81,10 @@ WKV_API int wkv_testing_pipe_rate(int pipe, int64_t iters, double* per_second,
   if (rc == WKV_OK && cudaEventRecord(e0, stream) != cudaSuccess) rc = WKV_ERR_CUDA;
   if (rc == WKV_OK) {
     if (pipe == WKV_PIPE_EX2)
-      ex2_probe_kernel<<<grid, kProbeThreads, 0, stream>>>(int(iters), sink);
+      rc = launch_kernel(ex2_probe_kernel, grid, kProbeThreads, 0, stream, int(iters), sink);
     else
-      ffma2_probe_kernel<<<grid, kProbeThreads, 0, stream>>>(int(iters), sink);
-    if (cudaPeekAtLastError() != cudaSuccess || cudaEventRecord(e1, stream) != cudaSuccess ||
+      rc = launch_kernel(ffma2_probe_kernel, grid, kProbeThreads, 0, stream, int(iters), sink);
+    if (rc != WKV_OK || cudaEventRecord(e1, stream) != cudaSuccess ||
         cudaEventSynchronize(e1) != cudaSuccess || cudaEventElapsedTime(&ms, e0, e1) != cudaSuccess ||
         ms <= 0.f)
       rc = WKV_ERR_CUDA;

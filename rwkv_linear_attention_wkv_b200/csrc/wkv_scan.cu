@@ -325,10 +325,9 @@ int launch_fwd_chunked_ex(const FwdArgs& a, void* scratch, int nseg, unsigned lo
       cudaSuccess)
     return WKV_ERR_CUDA;
   const int64_t grid = a.B * ((a.C + 31) / 32) * nseg;
-  kern<<<unsigned(grid), kW * 32, smem, stream>>>(tk, tv, tr, ty, int(a.B), int(a.T), int(a.C),
-                                                  nseg, a.w, a.u, a.a0, a.b0, a.p0, a.a1, a.b1,
-                                                  a.p1, scratch, a.err, wait_ns, withhold_seg0);
-  return cudaPeekAtLastError() == cudaSuccess ? WKV_OK : WKV_ERR_CUDA;
+  return launch_kernel(kern, unsigned(grid), kW * 32, smem, stream, tk, tv, tr, ty, int(a.B),
+                       int(a.T), int(a.C), nseg, a.w, a.u, a.a0, a.b0, a.p0, a.a1, a.b1, a.p1,
+                       scratch, a.err, wait_ns, withhold_seg0);
 }
 
 int launch_fwd_chunked(const FwdArgs& a, void* scratch, int nseg, cudaStream_t stream) {
