@@ -2,9 +2,10 @@
 // block: checks, allocations and the C call of one operator call, in one go. Each function takes
 // what its Python namesake (gdr.py, norm_gate.py) has checked nothing of, on the current stream,
 // and returns NotImplemented when anything at all is not as it should be; the Python function then
-// goes the long way, which explains the refusal or handles the unusual (another device, a status
-// other than WKV_OK). A decode call of one sequence costs 10 us the long way and 4 this way, two
-// of them the launch.
+// goes the long way, which explains the refusal or handles the unusual (another device). That is so
+// while nothing has been launched: a failure after that is raised from here, since a call that works
+// in place would do so twice. A decode call of one sequence costs 10 us the long way and 4 this way,
+// two of them the launch.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -22,8 +23,10 @@
 
 namespace {
 
-// Thrown for everything that is left to the long way.
+// Thrown for everything that is left to the long way: nothing has been launched.
 struct LongWay {};
+// Thrown with a Python error set.
+struct Raised {};
 
 using at::Tensor;
 
@@ -69,13 +72,33 @@ Tensor floats(at::IntArrayRef shape, const Tensor& like) {
 Tensor bytes(size_t n, const Tensor& like) {
   return at::empty({int64_t(n)}, like.options().dtype(at::kByte));
 }
-void done(int rc) {
-  if (rc != WKV_OK) throw LongWay();
+// The outcome of a call into the library: its refusals come before any launch, a CUDA error may
+// come after one.
+void done(const char* name, int rc) {
+  if (rc == WKV_OK) return;
+  if (rc != WKV_ERR_CUDA) throw LongWay();
+  PyObject* const module = PyImport_ImportModule("rwkv_linear_attention_wkv_b200");
+  PyObject* const type = module == nullptr ? nullptr : PyObject_GetAttrString(module, "WkvError");
+  PyObject* const error = type == nullptr ? nullptr : PyObject_CallFunction(type, "si", name, rc);
+  if (error != nullptr) PyErr_SetObject(type, error);
+  Py_XDECREF(error);
+  Py_XDECREF(type);
+  Py_XDECREF(module);
+  throw Raised();
+}
+// What is made of the results, after the call.
+PyObject* made(PyObject* o) {
+  if (o == nullptr) throw Raised();
+  return o;
 }
 PyObject* wrap(const Tensor& t) {
-  PyObject* o = THPVariable_Wrap(t);
-  if (o == nullptr) throw LongWay();
-  return o;
+  PyObject* o = nullptr;
+  try {
+    o = THPVariable_Wrap(t);
+  } catch (...) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "a result could not be wrapped");
+  }
+  return made(o);
 }
 // A given result checked, or a new one.
 Tensor result(PyObject* given, const Tensor& like, int dev) {
@@ -87,16 +110,18 @@ Tensor result(PyObject* given, const Tensor& like, int dev) {
 void put(PyObject* dict, const char* name, PyObject* value) {
   const int rc = PyDict_SetItemString(dict, name, value);
   Py_DECREF(value);
-  if (rc != 0) throw LongWay();
+  if (rc != 0) throw Raised();
 }
 PyObject* none() { Py_RETURN_NONE; }
 
-// Calls f and turns everything that goes wrong into the long way.
+// Calls f and turns everything that goes wrong before a launch into the long way.
 template <class F>
 PyObject* in_short(Py_ssize_t n, Py_ssize_t want, F f) {
   if (n == want) {
     try {
       return f();
+    } catch (const Raised&) {
+      return nullptr;
     } catch (...) {
       PyErr_Clear();
     }
@@ -162,7 +187,8 @@ PyObject* gdr_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* at_slots = tensor(a[6]);
     if (at_slots != nullptr) need(*at_slots, at::kInt, {r.p.B}, r.dev);
     const Tensor y = result(a[8], r.v, r.dev);
-    done(wkv_gdr_decode_step(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.v.data_ptr(), r.gp(), r.bp(),
+    done("wkv_gdr_decode_step",
+         wkv_gdr_decode_step(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.v.data_ptr(), r.gp(), r.bp(),
                              y.data_ptr(), static_cast<float*>(state.data_ptr()), slots,
                              static_cast<const int32_t*>(at_(at_slots)), stream_of(r.dev)));
     return wrap(y);
@@ -204,16 +230,18 @@ PyObject* forward(PyObject* const* a, bool keep) {
           kept.nbytes() < need_bytes)
         throw LongWay();
     }
-    done(wkv_gdr_forward_checkpointed(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.v.data_ptr(), r.gp(),
+    done("wkv_gdr_forward_checkpointed",
+         wkv_gdr_forward_checkpointed(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.v.data_ptr(), r.gp(),
                                       r.bp(), y.data_ptr(), s0, s1, kept.data_ptr(), kept.nbytes(),
                                       stream_of(r.dev)));
   } else {
-    done(wkv_gdr_forward(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.v.data_ptr(), r.gp(), r.bp(),
+    done("wkv_gdr_forward",
+         wkv_gdr_forward(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.v.data_ptr(), r.gp(), r.bp(),
                          y.data_ptr(), s0, s1, stream_of(r.dev)));
   }
   PyObject* const py = wrap(y);
   PyObject* const ps = want ? wrap(last) : none();
-  return keep ? Py_BuildValue("NNN", py, ps, wrap(kept)) : Py_BuildValue("NN", py, ps);
+  return made(keep ? Py_BuildValue("NNN", py, ps, wrap(kept)) : Py_BuildValue("NN", py, ps));
 }
 PyObject* gdr_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return in_short(n, 11, [&] { return forward(a, false); });
@@ -237,14 +265,14 @@ PyObject* gdr_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor ds;
     if (want) ds = floats(r.states(), r.v);
     const Tensor scratch = bytes(wkv_gdr_backward_workspace_bytes(&r.p), r.v);
-    done(wkv_gdr_backward(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.v.data_ptr(), r.gp(), r.bp(),
+    done("wkv_gdr_backward",
+         wkv_gdr_backward(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.v.data_ptr(), r.gp(), r.bp(),
                           dy.data_ptr(), kept.data_ptr(), kept.nbytes(), ds1, dq.data_ptr(),
                           dk.data_ptr(), dv.data_ptr(), static_cast<float*>(dg.data_ptr()),
                           static_cast<float*>(db.data_ptr()),
                           want ? static_cast<float*>(ds.data_ptr()) : nullptr, scratch.data_ptr(),
                           scratch.nbytes(), stream_of(r.dev)));
-    PyObject* const d = PyDict_New();
-    if (d == nullptr) throw LongWay();
+    PyObject* const d = made(PyDict_New());
     put(d, "dq", wrap(dq));
     put(d, "dk", wrap(dk));
     put(d, "dv", wrap(dv));
@@ -304,12 +332,13 @@ PyObject* norm_gate_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor out = result(a[9], m.h, m.dev);
     Tensor y;
     if (m.next_weight != nullptr) y = result(a[10], m.h, m.dev);
-    done(wkv_norm_gate_forward(&m.p, m.h.data_ptr(), m.fp(m.weight), at_(m.gate), at_(m.x),
+    done("wkv_norm_gate_forward",
+         wkv_norm_gate_forward(&m.p, m.h.data_ptr(), m.fp(m.weight), at_(m.gate), at_(m.x),
                                m.fp(m.scale), m.fp(m.next_weight), out.data_ptr(),
                                m.next_weight != nullptr ? y.data_ptr() : nullptr,
                                stream_of(m.dev)));
     PyObject* const po = wrap(out);
-    return Py_BuildValue("NN", po, m.next_weight != nullptr ? wrap(y) : none());
+    return made(Py_BuildValue("NN", po, m.next_weight != nullptr ? wrap(y) : none()));
   });
 }
 
@@ -330,12 +359,12 @@ PyObject* norm_gate_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor dh = at::empty_like(m.h), dw = like(m.weight), dz = like(m.gate), dx = like(m.x),
                  ds = like(m.scale), dn = dy == nullptr ? Tensor() : like(m.next_weight);
     const Tensor scratch = bytes(wkv_norm_gate_workspace_bytes(m.p.R, m.p.C), m.h);
-    done(wkv_norm_gate_backward(&m.p, m.h.data_ptr(), m.fp(m.weight), at_(m.gate), at_(m.x),
+    done("wkv_norm_gate_backward",
+         wkv_norm_gate_backward(&m.p, m.h.data_ptr(), m.fp(m.weight), at_(m.gate), at_(m.x),
                                 m.fp(m.scale), m.fp(m.next_weight), at_(dout), at_(dy),
                                 dh.data_ptr(), fptr(dw), ptr(dz), ptr(dx), fptr(ds), fptr(dn),
                                 scratch.data_ptr(), scratch.nbytes(), stream_of(m.dev)));
-    PyObject* const d = PyDict_New();
-    if (d == nullptr) throw LongWay();
+    PyObject* const d = made(PyDict_New());
     auto give = [&](const char* name, const Tensor& t) {
       put(d, name, t.defined() ? wrap(t) : none());
     };
