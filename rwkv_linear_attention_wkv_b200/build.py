@@ -15,6 +15,7 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -48,8 +49,15 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and not verbose_ptxas and up_to_date():
-        return LIB
+    """The library and, where torch is installed, the binding."""
+    if force or verbose_ptxas or not up_to_date():
+        build_library(verbose_ptxas)
+    if importlib.util.find_spec("torch") is not None:
+        build_binding(force)
+    return LIB
+
+
+def build_library(verbose_ptxas: bool = False) -> None:
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
            "-std=c++17", "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
            "--expt-relaxed-constexpr", "--threads", "0", "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp"]
@@ -58,19 +66,37 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     cmd += sources()
     subprocess.check_call(cmd)
     os.replace(LIB + ".tmp", LIB)
-    return LIB
+
+
+def torch_location() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def torch_version() -> str:
+    with open(os.path.join(torch_location(), "version.py")) as f:
+        return re.search(r"""__version__ = ['"](.+)['"]""", f.read()).group(1)
+
+
+def binding_up_to_date() -> bool:
+    """Newer than its sources, and built for the torch that is installed (it says so itself)."""
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    if any(os.path.getmtime(p) > t for p in [BINDING_SOURCE] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return False
+    with open(BINDING, "rb") as f:
+        return f"built for torch {torch_version()}\0".encode() in f.read()
 
 
 def build_binding(force: bool = False) -> str:
-    """After build(): it links against the library."""
-    newest = max(os.path.getmtime(p) for p in
-                 [BINDING_SOURCE] + glob.glob(os.path.join(INCLUDE, "*.h")))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+    """After build_library(): it links against the library."""
+    if not force and binding_up_to_date():
         return BINDING
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = torch_location()
     cuda = os.path.dirname(os.path.dirname(NVCC))
     subprocess.check_call(
-        [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+        [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+         f'-DTORCH_BUILT_FOR="{torch_version()}"', "-I", INCLUDE,
          "-I", os.path.join(torch, "include"), "-I", os.path.join(cuda, "include"),
          "-I", sysconfig.get_paths()["include"], BINDING_SOURCE, "-o", BINDING + ".tmp",
          "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
@@ -81,4 +107,3 @@ def build_binding(force: bool = False) -> str:
 
 if __name__ == "__main__":
     print(build(force=True, verbose_ptxas="--verbose-ptxas" in sys.argv))
-    print(build_binding(force=True))

@@ -389,4 +389,15 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&kModule); }
+// (build.py looks for these words, gdr.py compares the version with the torch that runs)
+const char kBuiltFor[] = "built for torch " TORCH_BUILT_FOR;
+
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* const m = PyModule_Create(&kModule);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version",
+                                                 kBuiltFor + sizeof("built for torch ") - 1) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

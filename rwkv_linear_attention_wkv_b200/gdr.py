@@ -7,20 +7,34 @@ caller made on another stream and lets go of before the call has run are the cal
 
 An ordinary call on the current stream goes through _binding.so (csrc/binding.cpp), which returns
 NotImplemented for whatever it does not take; the functions here then check, explain and call.
+They need libwkv.so alone.
 """
 from __future__ import annotations
 
 import ctypes
+import warnings
 
 import torch
 
-from . import LIB_PATH, WkvError, _made, lib
+from . import WkvError, _made, lib
+
+
+class _NoBinding:
+    """In the place of _binding.so: every call is left to the functions here."""
+
+    def __getattr__(self, name):
+        return lambda *args: NotImplemented
+
 
 try:
     from . import _binding
+    if getattr(_binding, "torch_version", None) != torch.__version__:
+        raise ImportError("it was built for another torch")
 except ImportError as e:
-    raise ImportError(f"{LIB_PATH[:-len('libwkv.so')]}_binding.so is missing or older than torch: "
-                      "build it with `python rwkv_linear_attention_wkv_b200/build.py`") from e
+    warnings.warn(f"_binding.so is not used ({e}): calls of the gated delta rule and the norms take a "
+                  "few microseconds longer; build it with "
+                  "`python rwkv_linear_attention_wkv_b200/build.py`", RuntimeWarning)
+    _binding = _NoBinding()
 
 _F32 = torch.float32
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
