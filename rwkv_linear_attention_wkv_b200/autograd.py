@@ -80,7 +80,7 @@ class GatedDeltaRuleFunction(torch.autograd.Function):
                      (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta))}
             if ctx.has_state:
                 H, N = v.shape[2:]
-                grads["dstate"] = torch.empty(seq_offsets.numel() - 1, H, N, N, device=v.device)
+                grads["dstate"] = v.new_empty(seq_offsets.numel() - 1, H, N, N, dtype=torch.float32)
         d = wkv_gdr_backward(q, k, v, g, beta, dy, workspace, grad_state=dlast, scale=ctx.scale,
                              seq_offsets=seq_offsets, want_dstate=ctx.has_state, grads=grads)
         return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], d["dstate"], None, None

@@ -1,0 +1,40 @@
+"""What the autograd functions meet in a program: another default type than fp32."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import gdr_reference as ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def run(x, state, off, dy, dS):
+    from rwkv_linear_attention_wkv_b200.autograd import gated_delta_rule
+    leaves = [t.detach().requires_grad_() for t in list(x) + [state]]
+    y, S = gated_delta_rule(*leaves[:5], state=leaves[5], scale=0.25, seq_offsets=off)
+    return [y, S] + list(torch.autograd.grad([y, S], leaves, [dy, dS]))
+
+
+@pytest.fixture(scope="module", params=[False, True], ids=["rows", "packed"])
+def case(request):
+    T, H, N = 50, 2, 64
+    off = torch.tensor([1, 20, 45], dtype=torch.int32, device="cuda") if request.param else None
+    n = 2 if request.param else 1
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = [t.cuda() for t in ref.inputs((1, T), 1, H, N, BF16, 2)]
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=FP32)  # noqa: E731
+    return x, 0.3 * r(n, H, N, N), off, r(1, T, H, N).to(BF16), r(n, H, N, N)
+
+
+@pytest.mark.parametrize("default", [BF16, torch.float64])
+def test_another_default_type(case, default):
+    want = run(*case)
+    torch.set_default_dtype(default)
+    try:
+        got = run(*case)
+    finally:
+        torch.set_default_dtype(FP32)
+    for a, b in zip(want, got):
+        assert a.dtype == b.dtype and torch.equal(a, b)
