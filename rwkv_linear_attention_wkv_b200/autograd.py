@@ -49,14 +49,22 @@ def wkv(w, u, k, v, r=None):
     return WKVFunction.apply(w, u, k, v, r)
 
 
+def _dense(t):
+    """t as the rule's kernels read it: contiguous, at a multiple of 16 bytes. A view or a gradient
+    may be contiguous and start anywhere."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class GatedDeltaRuleFunction(torch.autograd.Function):
     """(y, final states) of the gated delta rule with the library's gradients for q, k, v, g, beta
     and the initial states."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, state, scale, seq_offsets):
-        q, k, v, g, beta = (t.contiguous() for t in (q, k, v, g, beta))
-        state = None if state is None else state.contiguous()
+        q, k, v, g, beta, state = map(_dense, (q, k, v, g, beta, state))
         # tokens that no packed sequence covers are not written
         y = torch.empty_like(v) if seq_offsets is None else torch.zeros_like(v)
         y, last, workspace = wkv_gdr_forward_checkpointed(q, k, v, g, beta, state=state, scale=scale,
@@ -72,8 +80,8 @@ class GatedDeltaRuleFunction(torch.autograd.Function):
         if dy is None and dlast is None:
             return (None,) * 8
         q, k, v, g, beta, seq_offsets, workspace = ctx.saved_tensors
-        dy = torch.zeros_like(v) if dy is None else dy.contiguous()
-        dlast = None if dlast is None else dlast.contiguous()
+        dy = torch.zeros_like(v) if dy is None else _dense(dy)
+        dlast = _dense(dlast)
         grads = None
         if seq_offsets is not None:
             grads = {"d" + n: torch.zeros_like(t) for n, t in
@@ -89,7 +97,8 @@ class GatedDeltaRuleFunction(torch.autograd.Function):
 def gated_delta_rule(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None):
     """Differentiable wkv_gdr_forward: (y, final states), with gradients for q, k, v, g, beta and
     state, through both results. With seq_offsets, y and the gradients are zero at tokens that no
-    sequence covers. Types and shapes as wkv_gdr_forward; inputs may be non-contiguous."""
+    sequence covers. Types and shapes as wkv_gdr_forward; inputs may be non-contiguous and start
+    at any element."""
     return GatedDeltaRuleFunction.apply(q, k, v, g, beta, state, scale, seq_offsets)
 
 

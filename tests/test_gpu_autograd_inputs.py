@@ -1,4 +1,5 @@
-"""What the autograd functions meet in a program: another default type than fp32."""
+"""What the autograd functions are given in a program: tensors and gradients that are contiguous but
+start anywhere, and another default type than fp32."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -10,11 +11,19 @@ pytestmark = pytest.mark.gpu
 BF16, FP32 = torch.bfloat16, torch.float32
 
 
-def run(x, state, off, dy, dS):
+def shifted(t):
+    """A contiguous copy of t that starts one element behind an aligned address."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    out = buf[1:].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+def run(x, state, off, dy, dS, change=lambda t: t):
     from rwkv_linear_attention_wkv_b200.autograd import gated_delta_rule
-    leaves = [t.detach().requires_grad_() for t in list(x) + [state]]
+    leaves = [change(t.detach()).requires_grad_() for t in list(x) + [state]]
     y, S = gated_delta_rule(*leaves[:5], state=leaves[5], scale=0.25, seq_offsets=off)
-    return [y, S] + list(torch.autograd.grad([y, S], leaves, [dy, dS]))
+    return [y, S] + list(torch.autograd.grad([y, S], leaves, [change(dy), change(dS)]))
 
 
 @pytest.fixture(scope="module", params=[False, True], ids=["rows", "packed"])
@@ -26,6 +35,11 @@ def case(request):
     x = [t.cuda() for t in ref.inputs((1, T), 1, H, N, BF16, 2)]
     r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=FP32)  # noqa: E731
     return x, 0.3 * r(n, H, N, N), off, r(1, T, H, N).to(BF16), r(n, H, N, N)
+
+
+def test_tensors_that_start_anywhere(case):
+    for a, b in zip(run(*case), run(*case, change=shifted)):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("default", [BF16, torch.float64])
