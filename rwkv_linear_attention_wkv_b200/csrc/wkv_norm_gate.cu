@@ -278,11 +278,17 @@ __device__ __forceinline__ Eight inverse_rms(const Eight& sum, float inv, float 
   return r;
 }
 
-// sigmoid(z) by the exponential and reciprocal instructions: e^-z is off by |z| 2^-24 of itself,
-// the sigmoid by at most s (1 - s) |z| 2^-24 < 2^-26. (expf and a division: 15 instructions more,
-// a third of a forward row.)
-__device__ __forceinline__ float sigmoid_of(float z) {
-  return rcp(1.f + ex2(z * -1.4426950408889634f));
+// e^-z by the exponential instruction: off by less than |z| 2^-23 of itself, the roundings of its
+// argument and of log2(e), and by the instruction's 2^-22.
+__device__ __forceinline__ float exp_minus(float z) { return ex2(z * -1.4426950408889634f); }
+
+// s = sigmoid(z) by the exponential and reciprocal instructions: 1 - s times what e^-z is off by, the
+// sum's rounding of 2^-24 and the reciprocal's 2^-23; 2^-21 of s at most for z >= 0, |z| 2^-23 more
+// below. (expf and a division: 15 instructions more, a third of a forward row.)
+__device__ __forceinline__ float sigmoid_of(float z) { return rcp(1.f + exp_minus(z)); }
+// 1 - sigmoid(z) from s = sigmoid(z), without the difference where s is close to one.
+__device__ __forceinline__ float off_of(float z, float s) {
+  return z > 0.f ? exp_minus(z) * s : 1.f - s;
 }
 
 template <bool VEC>
@@ -419,9 +425,10 @@ __global__ void __launch_bounds__(MAX_THREADS, 1) norm_gate_bwd_kernel(NormGateA
     if (a.dgate) {
       // silu' = sig + z sig (1 - sig), sigmoid' = sig (1 - sig)
       Eight slope;
+      const Eight zv = widen<T>(zk);
 #pragma unroll
       for (int i = 0; i < kE; ++i) {
-        const float off = 1.f - sig.v[i];
+        const float off = off_of(zv.v[i], sig.v[i]);
         slope.v[i] = silu ? ::fmaf(act.v[i], off, sig.v[i]) : sig.v[i] * off;
       }
       store<T, VEC>(static_cast<T*>(a.dgate) + row * a.C, n * hn * slope, pl);
