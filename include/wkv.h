@@ -334,7 +334,8 @@ WKV_API int wkv_mstate_forward(int64_t B, int64_t T, int64_t H, int64_t N, const
  * the tokens [seq_offsets[s], seq_offsets[s + 1]). Offsets are clamped to [0, T] and a
  * sequence that ends before it starts is empty; sequences must not overlap. Tokens that no
  * sequence covers are not read, and their rows of the outputs stay as they were.
- * N must be 64 or 128 and Hk must divide H (else WKV_ERR_UNSUPPORTED); q, k, v, y and the
+ * N must be 64 or 128, Hk must divide H and T must not exceed 2^31 - 1024 (else
+ * WKV_ERR_UNSUPPORTED); q, k, v, y and the
  * states must be 16-byte aligned, g, beta and seq_offsets 4-byte (else WKV_ERR_ALIGNMENT).
  * Stable for |beta_t| |k_t|^2 <= 2 (keys are unit vectors in a model). Inputs finite (but g,
  * above): a value that is not reaches the tokens of its own 16-token group and all later ones.

@@ -27,9 +27,10 @@ int check_problem(const wkv_gdr_problem* p, bool* empty) {
   }
   if (p->N != 64 && p->N != 128) return WKV_ERR_UNSUPPORTED;
   if (p->Hk == 0 || p->H % p->Hk != 0) return WKV_ERR_UNSUPPORTED;
-  // Tokens and heads are indexed in int32, elements in int64; a grid is 31 bits wide.
+  // Tokens (rounded up to a kernel's step, or to what segments there may be) and heads are indexed in
+  // int32, elements in int64; a grid is 31 bits wide.
   constexpr int64_t kMax = int64_t(1) << 31;
-  if (p->T >= kMax || p->H >= (int64_t(1) << 20) || p->B >= kMax || seqs >= kMax / 8 / p->H)
+  if (p->T > kMax - 1024 || p->H >= (int64_t(1) << 20) || p->B >= kMax || seqs >= kMax / 8 / p->H)
     return WKV_ERR_UNSUPPORTED;
   if (p->T > 0 && (p->B > (int64_t(1) << 40) / p->T ||
                    p->B * p->T > INT64_MAX / 16 / (p->H * p->N)))
