@@ -21,7 +21,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (wkv_backward_checkpointed, wkv_forward_checkpointed, wkv_gdr_backward,
-               wkv_gdr_forward_checkpointed, wkv_norm_gate_backward, wkv_norm_gate_forward)
+               wkv_gdr_forward, wkv_gdr_forward_checkpointed, wkv_norm_gate_backward,
+               wkv_norm_gate_forward)
 
 
 class WKVFunction(torch.autograd.Function):
@@ -58,6 +59,11 @@ def _dense(t):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+def _read_outs(v, seq_offsets):
+    # tokens that no packed sequence covers are not written
+    return torch.empty_like(v) if seq_offsets is None else torch.zeros_like(v)
+
+
 class GatedDeltaRuleFunction(torch.autograd.Function):
     """(y, final states) of the gated delta rule with the library's gradients for q, k, v, g, beta
     and the initial states."""
@@ -65,8 +71,7 @@ class GatedDeltaRuleFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, beta, state, scale, seq_offsets):
         q, k, v, g, beta, state = map(_dense, (q, k, v, g, beta, state))
-        # tokens that no packed sequence covers are not written
-        y = torch.empty_like(v) if seq_offsets is None else torch.zeros_like(v)
+        y = _read_outs(v, seq_offsets)
         y, last, workspace = wkv_gdr_forward_checkpointed(q, k, v, g, beta, state=state, scale=scale,
                                                           seq_offsets=seq_offsets, y=y)
         ctx.save_for_backward(q, k, v, g, beta, seq_offsets, workspace)
@@ -99,7 +104,13 @@ def gated_delta_rule(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None):
     state, through both results. With seq_offsets, y and the gradients are zero at tokens that no
     sequence covers. Types and shapes as wkv_gdr_forward; inputs may be non-contiguous and start
     at any element."""
-    return GatedDeltaRuleFunction.apply(q, k, v, g, beta, state, scale, seq_offsets)
+    inputs = (q, k, v, g, beta, state)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        return GatedDeltaRuleFunction.apply(*inputs, scale, seq_offsets)
+    # nothing to keep for a backward (every token's error and the chunks' states: more than the inputs)
+    q, k, v, g, beta, state = map(_dense, inputs)
+    return wkv_gdr_forward(q, k, v, g, beta, state=state, scale=scale, seq_offsets=seq_offsets,
+                           y=_read_outs(v, seq_offsets))
 
 
 class NormGateFunction(torch.autograd.Function):

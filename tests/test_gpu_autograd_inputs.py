@@ -1,5 +1,5 @@
-"""What the autograd functions are given in a program: tensors and gradients that are contiguous but
-start anywhere, and another default type than fp32."""
+"""What the autograd functions meet in a program: tensors and gradients that are contiguous but start
+anywhere, another default type than fp32, and calls that no backward follows."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -40,6 +40,23 @@ def case(request):
 def test_tensors_that_start_anywhere(case):
     for a, b in zip(run(*case), run(*case, change=shifted)):
         assert torch.equal(a, b)
+
+
+def test_nothing_is_kept_without_a_backward(case):
+    from rwkv_linear_attention_wkv_b200.autograd import gated_delta_rule
+    x, state, off, dy, dS = case
+    want = run(*case)[:2]
+    leaves = [t.detach().requires_grad_() for t in x]
+    for grad, ins in ((False, leaves), (True, x)):
+        with torch.set_grad_enabled(grad):
+            torch.cuda.synchronize()
+            torch.cuda.reset_peak_memory_stats()
+            before = torch.cuda.memory_allocated()
+            got = gated_delta_rule(*ins, state=state, scale=0.25, seq_offsets=off)
+            used = torch.cuda.max_memory_allocated() - before
+        assert all(torch.equal(a, b) and not b.requires_grad for a, b in zip(want, got))
+        # the results alone, in blocks of 512 bytes
+        assert used <= sum(t.numel() * t.element_size() + 512 for t in got), used
 
 
 @pytest.mark.parametrize("default", [BF16, torch.float64])
