@@ -2,23 +2,25 @@
 // parts of fp32 values, the tokens' tiles in shared memory, and the small matrices of a group
 // of 16 tokens.
 //
-// Why warp matrix instructions (mma.sync) and not tcgen05 here. A head's state is N x N and every
-// product of the rule has a side of 64 or 128 and one of 16 tokens; the results feed the next
-// product at once. With mma.sync the state stays in a warp's registers as the accumulator of one
-// product and, since an accumulator tile and an operand tile are laid out alike, turns into the
-// operand of the next by splitting it in place. tcgen05 would take every operand through shared
-// memory (split, stored, fenced, waited for) twice a chunk: the matrix-state kernel, which does
-// that with 64-token chunks, spends 34,000 cycles a chunk of which the tensor pipe is busy a
-// sixth. mma.sync m16n8k16 runs at 549 TFLOP/s here (8 cycles an instruction and scheduler), a
-// third of tcgen05's rate, and the rule at 16 tokens a group needs no more than the chain of
-// latencies leaves time for.
+// Warp matrix instructions (mma.sync). A head's state is N x N and every product of the rule has a
+// side of 64 or 128 and one of 16 tokens; the results feed the next product at once. The state stays
+// in a warp's registers as the accumulator of one product and, since an accumulator tile and an
+// operand tile are laid out alike, turns into the operand of the next by splitting it in place, and
+// so do the group's small matrices. mma.sync m16n8k16 runs at 549 TFLOP/s here (8 cycles an
+// instruction and scheduler), a third of tcgen05's rate; few heads are bound by the chain of a
+// group's products, many by issue slots. tcgen05 takes its first operand from tensor memory, where
+// the state could stay as well (tf32: the high part in place, the rest as a second operand), in
+// chunks of 64 tokens; that form is not built and not measured here. (The matrix-state kernel, which
+// takes every operand through shared memory, keeps the tensor pipe busy a sixth of the time: a
+// property of its phases, one after the other, not of the unit.)
 //
 // Precision: a state, and what is derived from it, is fp32; as an operand it is split into three
 // bf16 parts (24 bits), so that products with bf16 inputs (one part) take 3 instructions and
 // products of two split values 6 (hi hi, hi mid, mid hi, hi lo, lo hi, mid mid: what is left out is
 // below 2^-22). fp32 inputs are split into three parts as well. So a bf16 result is an fp32 result
 // rounded once. (The read-outs of bf16 problems with two parts a factor, 2^-15 of a value: 754 us
-// instead of 843 at 8 x 4096 x 64 x 64, and six times as many of them on the other side of a rounding.)
+// instead of 848 at 8 x 4096 x 64 x 64, and forty times as many of them on the other side of a
+// rounding.)
 #pragma once
 
 #include <cstdint>
@@ -75,9 +77,10 @@ __device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) {
 // Two values as three packed bf16 parts that add up to them, 8 bits each: mid and lo by cutting
 // off, hi to the nearest, or cut off as well (CUT: two instructions less, for operands of a product
 // with exact bf16 values, where no part pair is left out; two parts are then good to 2^-15). With
-// integer adds, masks and byte permutes: packed conversions and fp32x2 arithmetic take as many instructions, but wait for one another and for the matrix
-// instructions (16 such splits beside 16 matrix instructions, cycles a scheduler: 435 with
-// conversions, 298 this way; 129 for the matrix instructions alone).
+// integer adds, masks and byte permutes: packed conversions and fp32x2 arithmetic take as many
+// instructions, but wait for one another and for the matrix instructions (16 such splits beside 16
+// matrix instructions, cycles a scheduler: 435 with conversions, 298 this way; 129 for the matrix
+// instructions alone).
 template <bool CUT = false>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& mid,
                                        uint32_t& lo) {
@@ -196,7 +199,7 @@ __device__ __forceinline__ int64_t sequence(const GdrArgs& a, int seq, int& len)
 
 // The sequence that comes `rank`-th when the longest come first: a walk is as long as its sequence,
 // and a long one that starts last leaves the SMs idle (17 sequences of 9001 tokens, 32 x 128 heads:
-// 466 us, 368 longest first). Up to 64 packed sequences; more are taken as they come. Whole warps.
+// 428 us, 330 longest first). Up to 64 packed sequences; more are taken as they come. Whole warps.
 __device__ __forceinline__ int by_length(const GdrArgs& a, int rank, int lane) {
   if (a.offsets == nullptr || a.n_seqs > 64) return rank;
   int len[2] = {-1, -1}, before[2] = {0, 0};
@@ -650,9 +653,9 @@ __device__ __forceinline__ bool start_state(float (&S)[N / 8][4], const GdrArgs&
 
 // Four consumers and steps of two groups everywhere (heads of 128 are two CTAs). bf16: two
 // producers, 168 registers and two CTAs an SM where there is work for them, or four producers and
-// one CTA, which is quicker alone (us, singles / pairs: 1 x 2048 x 8 x 64: 129 / 114, 1 x 2048 x 8
-// x 128: 199 / 168) and slower where CTAs queue (8 x 4096 x 64 x 64: 785 / 881, 16 x 1024 x 32 x
-// 128: 561 / 599). fp32 splits q and k on the way, which takes four producers always (two / four:
+// one CTA, which is quicker alone (us, singles / pairs: 1 x 2048 x 8 x 64: 134 / 119, 1 x 2048 x 8
+// x 128: 203 / 177) and slower where CTAs queue (8 x 4096 x 64 x 64: 849 / 932, 16 x 1024 x 32 x
+// 128: 587 / 625). fp32 splits q and k on the way, which takes four producers always (two / four:
 // 8 x 1024 x 64 x 64: 496 / 379, 1 x 2048 x 8 x 64: 253 / 186).
 enum GdrWalkForm { kGdrWalkSingles, kGdrWalkPairs, kGdrWalkError };
 inline GdrWalkForm gdr_walk_form(const GdrArgs& a, int64_t spans) {

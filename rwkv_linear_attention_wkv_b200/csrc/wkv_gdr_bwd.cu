@@ -27,10 +27,11 @@
 // an fp32 gradient rounded once. What only the bf16 dk sees is added up by the matrix instructions
 // alone (see product()).
 //
-// Measured, 16 x 1024 x 12 x 64 bf16: chain 122 us, second kernel 196 us. The chain is bound like
-// the forward (wkv_gdr_fwd.cu). The second kernel issues a third of the time and has its matrix
-// pipe busy a quarter: 16 warps an SM wait for each other's tiles (barriers) and for e, du and
-// states, 2 KB a token and head, which HBM delivers in 55 us.
+// Measured, 16 x 1024 x 12 x 64 bf16: chain 127 us, second kernel 275 us (198 with two parts for dk
+// and dg from the running sums). The chain is bound like the forward (wkv_gdr_fwd.cu). The second
+// kernel issues a third of the time and has its matrix pipe busy a third: 16 warps an SM wait for
+// each other's tiles (barriers) and for e, du and states, 1.6 KB a token and head, which HBM
+// delivers in 50 us.
 #include "wkv_gdr.cuh"
 
 namespace wkv {

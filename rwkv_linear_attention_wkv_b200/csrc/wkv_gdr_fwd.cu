@@ -9,10 +9,11 @@
 // registers, and the products run transposed (channels x tokens): S_0 K^T and S_0 Q^T take the
 // state as operand a in place, e^T and the weighted e^T become operands as they come out.
 //
-// Bound by issue slots: a group of a head takes 2,960 warp instructions, 400 of them matrix
+// Bound by issue slots: a group of a head takes 3,080 warp instructions, 400 of them matrix
 // instructions of 8 cycles that hold the issue port for about 4.5, so that the matrix time adds to
-// the rest instead of hiding behind it (8 x 4096 x 64 x 64 bf16: 843 us, 0.20 of HBM). More warps do
-// not help (three CTAs of 96 registers took 8 % longer), fewer instructions do.
+// the rest instead of hiding behind it (8 x 4096 x 64 x 64 bf16: 848 us, matrix pipe half busy,
+// 0.20 of HBM). More warps do not help (three CTAs of 96 registers took 8 % longer), fewer
+// instructions do.
 // Few heads are bound by a group's chain of products, 0.9 us (bf16, 64): see wkv_gdr_seg.cu.
 //
 // A CTA has 64 value channels of one head of one sequence (or of a segment of it): two or four

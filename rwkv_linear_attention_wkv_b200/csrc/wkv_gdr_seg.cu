@@ -7,10 +7,10 @@
 // outputs. Three times the work of one pass, over as many times the CTAs. The reverse walk is the
 // same with the segments in the other order (its M is the transpose).
 //
-// Measured, 1 x 16384 x 8 x 64 fp32 in 18 segments: 149 + 39 + 97 us against 1,480 whole. With
-// four segments a sequence (the fewest taken), whole / in segments, us: 1 x 1024 x 8 x 64 bf16 84 /
-// 77, fp32 112 / 81; 1 x 4096 x 37 x 64 bf16 251 / 186; 1 x 2048 x 16 x 128 bf16 191 / 172; 1 x 1024
-// x 18 x 128 bf16 104 / 112.
+// Measured, 1 x 16384 x 8 x 64 fp32 in 18 segments: 151 + 41 + 99 us against 1,480 whole. With
+// four segments a sequence (the fewest taken), whole / in segments, us: 1 x 1024 x 8 x 64 bf16 62 /
+// 46, fp32 95 / 60; 1 x 4096 x 37 x 64 bf16 235 / 157; 1 x 2048 x 16 x 128 bf16 178 / 141; 1 x 1024
+// x 18 x 128 bf16 92 / 88.
 #include <algorithm>
 
 #include "wkv_gdr.cuh"
@@ -133,9 +133,9 @@ int64_t gdr_plan_segments(const GdrArgs& a, GdrSegs* segs) {
   const bool packed = a.offsets != nullptr;
   if (packed && a.n_seqs > 64) return 0;  // find_span
   // Packed lengths are not known here: one span a sequence, the rest cut from whatever is long.
-  // Where nothing is, every sequence is one span, and the two other passes cost 15 us for nothing;
-  // so they have to be short enough for twice the gain. (16 x 64, whole / in segments, us: 3700,
-  // 100, 100 and 100 tokens bf16 219 / 133, fp32 353 / 180; four of 1000 bf16 75 / 90.)
+  // Where nothing is, every sequence is one span, and the two other passes are for nothing; so they
+  // have to be short enough for twice the gain. (8 x 64, whole / in segments, us: 3700, 100, 100 and
+  // 100 tokens bf16 211 / 82, fp32 328 / 115; four of 1000 bf16 62 / 64, fp32 95 / 97.)
   const int want = packed ? cap - a.n_seqs : cap / a.n_seqs, least = packed ? 2 * kGain : kGain;
   if (want < least) return 0;
   int tokens = (a.T + want - 1) / want;

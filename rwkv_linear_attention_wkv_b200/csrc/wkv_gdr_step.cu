@@ -6,8 +6,8 @@
 // its own columns. 16 lanes hold a row, a warp 16 rows (two at a time), all of them loaded
 // before the first is used, so that a warp has its 4 KiB (N = 64) or 8 KiB (N = 128) of state
 // in flight at once. Bound by HBM: a token reads and writes the state once, 8 N^2 bytes a head
-// against 6 N^2 flops. Measured: 256 rows x 64 heads x 64, fp32: 86 us, 0.98 of the copy rate;
-// 87 rows of a pool x 32 x 128, bf16: 61 us, 0.91; one row of 12 heads: 4 us, the launch.
+// against 6 N^2 flops. Measured: 256 rows x 64 heads x 64, fp32: 87 us, 0.96 of the copy rate;
+// 87 rows of a pool x 32 x 128, bf16: 62 us, 0.91; one row of 12 heads: 4 us, the launch.
 #include "wkv_device.cuh"
 #include "wkv_internal.h"
 

@@ -13,9 +13,9 @@
 // before this row's sums, so that a row is always in flight. Group sums are shuffles where a group
 // is 8 x a power of two channels up to 256 (the heads), the row sum where it is the row, and go
 // through shared memory otherwise.
-// Bound by HBM: 32768 x 4096 bf16 with gate, residual and next norm in 255 us, 5.3 TB/s, 0.80 of
-// the copy rate. The backward (16384 x 768 in 56 us, 3.6 TB/s) by latency: its sums leave 12 warps
-// an SM. Few rows by the launch (256 x 4096: 6 us).
+// Bound by HBM: 32768 x 4096 bf16 with gate, residual and next norm in 267 us, 5.0 TB/s, 0.76 of
+// the copy rate; 16384 x 4096 fp32 in 230 us, 0.89. The backward (16384 x 768 in 58 us, 3.5 TB/s) by
+// latency: its sums leave 12 warps an SM. Few rows by the launch (256 x 4096: 6 us).
 #include <algorithm>
 
 #include "wkv_device.cuh"
@@ -516,7 +516,8 @@ Plan plan_of(int64_t R, int C, int group, bool vec, bool bf16, bool backward, in
 
 // Backward: rows of up to 12 warps fit 384 threads, which leaves a thread 168 registers for
 // the sums over rows, this row and the next; up to 16 warps take 512 threads and 128; wider
-// ones take 1024 threads and spill.
+// ones take 1024 threads and spill (forward and backward of 4096 x 4096 bf16: 156 us, 0.33 of HBM;
+// of 2048 x 8192: 339 us, 0.15).
 template <typename T, bool VEC, GroupMode MODE>
 int run(const NormGateArgs& a, const Plan& p, bool backward, cudaStream_t stream) {
   const int warps = p.team_warps * p.teams;
