@@ -178,7 +178,8 @@ def wkv_gdr_forward(q, k, v, g, beta, state=None, scale=1.0, seq_offsets=None, y
 
     seq_offsets (int32, n + 1) packs n sequences into one row (B = 1). state: (sequences, H,
     N, N) fp32 or None (zero). Returns (y, S_T), or (y, None) with want_state=False. state_out
-    may be `state` itself.
+    may be `state` itself. Rows of y that no packed sequence covers are left as they were
+    (uninitialised without `y`).
     """
     if stream is None:
         done = _binding.gdr_forward(q, k, v, g, beta, state, scale, seq_offsets, y, state_out,
@@ -277,7 +278,7 @@ def wkv_gdr_decode_step(q, k, v, g, beta, state, slots=None, scale=1.0, y=None, 
 
     state: (slots, H, N, N) fp32, updated in place; slots: int32 (n,), the state of each row
     (no slot twice; outside [0, len(state)): padding, the row is skipped and its y stays as it
-    was), None = row i has state i. Returns y (n, H, N).
+    was, uninitialised without `y`), None = row i has state i. Returns y (n, H, N).
     """
     if stream is None:
         done = _binding.gdr_decode(q, k, v, g, beta, state, slots, scale, y)
